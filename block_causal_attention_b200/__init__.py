@@ -14,7 +14,7 @@ import numpy as np
 from . import _abi
 from ._abi import BcaError  # noqa: F401
 
-__all__ = ["Plan", "BcaError"]
+__all__ = ["Plan", "PagedCache", "PagePool", "BcaError"]
 
 
 def _ptr(t) -> Optional[int]:
@@ -248,3 +248,6 @@ class Plan:
             self.close()
         except Exception:
             pass
+
+
+from .paged import PagedCache, PagePool  # noqa: E402,F401

@@ -21,6 +21,7 @@ BCA_ERR_DEVICE_TIMEOUT = -6
 BCA_ERR_HOST_ONLY_PLAN = -7
 BCA_ERR_NO_MEMORY = -8
 BCA_ERR_TOO_LARGE = -9
+BCA_ERR_BAD_PAGE = -10
 BCA_STATIC_WORKSPACE_BYTES = 16 << 20
 
 BCA_SLICE_FULL = 0
@@ -32,6 +33,8 @@ BCA_FWD_FP8_E4M3 = 0x8
 BCA_NO_PROLOGUE = 0x10
 BCA_DQ_DETERMINISTIC = 0x20
 BCA_CACHE_K_FP16 = 0x40
+BCA_PAGED_FP16 = 0x80
+BCA_PAGE_TOKENS = 128
 BCA_PASS_FWD = 0
 BCA_PASS_BWD = 1
 
@@ -41,7 +44,9 @@ EXPORTS = ("bca_plan_create", "bca_plan_destroy", "bca_plan_get_info", "bca_plan
            "bca_plan_update_positions", "bca_workspace_bytes", "bca_fwd", "bca_fwd_static_workspace", "bca_bwd",
            "bca_bwd_ex", "bca_attn_merge", "bca_k_prologue", "bca_k_prologue_bwd",
            "bca_profile_enable",
-           "bca_profile_read", "bca_status", "bca_error_string")
+           "bca_profile_read", "bca_status", "bca_paged_create", "bca_paged_destroy", "bca_paged_pool_bytes",
+           "bca_paged_write", "bca_paged_copy", "bca_paged_workspace_bytes", "bca_paged_attend",
+           "bca_paged_status", "bca_error_string")
 BCA_KERNEL_KV_IMAGE = 0
 BCA_KERNEL_FWD = 1
 KERNEL_NAMES = {0: "kv_image_kernel", 1: "fwd_kernel", 2: "bwd_prep_kernel", 3: "bwd_kv_image_kernel",
@@ -65,6 +70,12 @@ class bca_problem(ctypes.Structure):
                 ("num_slices", ctypes.c_int32), ("slices", ctypes.c_void_p),
                 ("rope_base", ctypes.c_float * 3), ("norm_eps", ctypes.c_float),
                 ("flags", ctypes.c_uint32)]
+
+
+class bca_paged_desc(ctypes.Structure):
+    _fields_ = [("num_q_heads", ctypes.c_int32), ("num_kv_heads", ctypes.c_int32),
+                ("head_dim", ctypes.c_int32), ("num_layers", ctypes.c_int32), ("num_pages", ctypes.c_int64),
+                ("rope_base", ctypes.c_float * 3), ("norm_eps", ctypes.c_float), ("flags", ctypes.c_uint32)]
 
 
 class bca_plan_info(ctypes.Structure):
@@ -127,6 +138,23 @@ def lib() -> ctypes.CDLL:
         L.bca_profile_read.restype = i32
         L.bca_status.argtypes = [vp, vp]
         L.bca_status.restype = i32
+        L.bca_paged_create.argtypes = [ctypes.POINTER(bca_paged_desc), ctypes.POINTER(vp)]
+        L.bca_paged_create.restype = i32
+        L.bca_paged_destroy.argtypes = [vp]
+        L.bca_paged_destroy.restype = None
+        L.bca_paged_pool_bytes.argtypes = [vp]
+        L.bca_paged_pool_bytes.restype = ctypes.c_size_t
+        L.bca_paged_write.argtypes = [vp, vp, vp, i64, vp, vp, vp, i32, i32, vp, vp, vp, vp, vp]
+        L.bca_paged_write.restype = i32
+        L.bca_paged_copy.argtypes = [vp, vp, i64, vp, vp, vp]
+        L.bca_paged_copy.restype = i32
+        L.bca_paged_workspace_bytes.argtypes = [vp, i64, i32]
+        L.bca_paged_workspace_bytes.restype = ctypes.c_size_t
+        L.bca_paged_attend.argtypes = [vp, vp, i64, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, vp,
+                                       vp, vp]
+        L.bca_paged_attend.restype = i32
+        L.bca_paged_status.argtypes = [vp, vp]
+        L.bca_paged_status.restype = i32
         L.bca_error_string.argtypes = [i32]
         L.bca_error_string.restype = ctypes.c_char_p
         _lib = L

@@ -392,6 +392,7 @@ const char *bca_error_string(int code) {
         case BCA_ERR_HOST_ONLY_PLAN: return "plan was built host-only (BCA_PLAN_HOST_ONLY)";
         case BCA_ERR_NO_MEMORY: return "out of memory";
         case BCA_ERR_TOO_LARGE: return "problem needs more scratch than the static workspace holds";
+        case BCA_ERR_BAD_PAGE: return "a token without a page, or a page move that is not allowed";
         default: return "unknown error";
     }
 }

@@ -1,0 +1,441 @@
+// The paged KV cache on sm_100a: writing new tokens into pages, copying pages, and the
+// launches of attention over pages (paged_rows.cu, paged_tiles.cu) with the pass that joins
+// the pieces of items that several blocks shared.
+#include <cuda_runtime.h>
+
+#include <algorithm>
+#include <cstring>
+#include <type_traits>
+
+#include "paged_device.cuh"
+
+namespace bca {
+
+namespace {
+
+// ------------------------------------------------------------------ writing new tokens
+//
+// k_hat = R(pos) (gain * k / sqrt(mean k^2 + eps)) in fp16, v as it is, both into the layout
+// of the pages.  Bound by memory: 4 D Hkv bytes read and as many written a token.
+//
+// A block takes the (up to) 32 tokens of one 32-aligned stretch of a page, all KV heads: the
+// angles (64-bit turns, sine and cosine) are computed once a token instead of once a head.
+// Eight lanes share a key row (one 16-byte chunk each, D / 8 of them at work), four
+// neighbouring tokens a warp, so that the stores of a chunk are 64 contiguous bytes.  A value
+// is written as the 16 bytes of eight neighbouring tokens (a whole row of the V layout) where
+// the call has all eight, else as single values: the other slots are not this call's.
+
+constexpr int kWriteTokens = 32;
+constexpr int kWriteThreads = 256;
+
+struct WriteArgs {
+    const void *k, *v;
+    const int32_t *pos;
+    const float *k_gain;
+    const int32_t *table, *off, *start;
+    __half *k_pages;
+    void *v_pages;
+    int *status;
+    int64_t n, pages;
+    int seqs, width, hkv;
+    float eps;
+    double turns[24];
+};
+
+// The block of 32-aligned tokens that this grid block has.  Sequence b begins at grid block
+// off[b] / 32 + 2 b: tokens that need not begin at a multiple of 32 touch at most n / 32 + 2
+// stretches, which is what is left before sequence b + 1.
+struct WriteTile {
+    int64_t row;   // of the first token
+    int64_t at;    // its position in the sequence
+    int count;     // tokens
+    int b;
+};
+
+__device__ __forceinline__ bool write_tile(const WriteArgs &a, WriteTile &t) {
+    const int64_t x = blockIdx.x;
+    int before = 0;
+    for (int base = 0; base < a.seqs; base += kWriteThreads) {
+        const int b = base + (int)threadIdx.x;
+        const bool in = b < a.seqs && min(max((int64_t)__ldg(a.off + b), (int64_t)0), a.n) / kWriteTokens + 2 * (int64_t)b <= x;
+        const int c = __syncthreads_count(in);
+        before += c;
+        if (c < kWriteThreads) break;
+    }
+    if (before == 0) return false;
+    t.b = before - 1;
+    const int64_t o0 = min(max((int64_t)__ldg(a.off + t.b), (int64_t)0), a.n);
+    const int64_t o1 = min(max((int64_t)__ldg(a.off + t.b + 1), o0), a.n);
+    const int64_t s = __ldg(a.start + t.b);
+    const int64_t first = ((s >> 5) + (x - (o0 / kWriteTokens + 2 * (int64_t)t.b))) * kWriteTokens;
+    const int64_t lo = max(first, s), hi = min(first + kWriteTokens, s + (o1 - o0));
+    if (lo >= hi) return false;
+    t.at = lo;
+    t.row = o0 + (lo - s);
+    t.count = (int)(hi - lo);
+    return true;
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const __grid_constant__ WriteArgs a) {
+    constexpr int P = Geo<D>::PAIRS;
+    constexpr int C = D / 8;
+    __shared__ float2 turn[kWriteTokens][3 * P];
+    WriteTile t;
+    if (!write_tile(a, t)) return;
+    const int64_t page_at = t.at / kPage;
+    int64_t page = -1;
+    if (t.at >= 0 && page_at < a.width) page = __ldg(a.table + (int64_t)t.b * a.width + page_at);
+    if (page < 0 || page >= a.pages) {
+        if (threadIdx.x == 0) atomicOr(a.status, kPagedNoPage);
+        return;
+    }
+    const int slot = (int)(t.at % kPage);
+    if (a.pos) {
+        for (int u = threadIdx.x; u < t.count * 3 * P; u += kWriteThreads) {
+            const int tok = u / (3 * P), p = u % (3 * P), axis = p / P;
+            turn[tok][p] = paged_cos_sin(__ldg(a.pos + (t.row + tok) * 3 + axis), a.turns[8 * axis + p - axis * P]);
+        }
+        __syncthreads();
+    }
+
+    // keys
+    const T *k = static_cast<const T *>(a.k);
+    const int fours = (t.count + 3) / 4;
+    const int e = threadIdx.x % 8;
+    float gain[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) gain[i] = a.k_gain && e < C ? __ldg(a.k_gain + 8 * e + i) : 1.f;
+    for (int u = threadIdx.x / 8; u < fours * a.hkv * 4; u += kWriteThreads / 8) {
+        const int head = u / 4 % a.hkv, tok = u / 4 / a.hkv * 4 + u % 4;
+        const bool on = tok < t.count && e < C;
+        float x[8];
+        uint4 raw = make_uint4(0, 0, 0, 0);
+        if (on) raw = __ldg(reinterpret_cast<const uint4 *>(k + ((t.row + tok) * a.hkv + head) * D) + e);
+        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = Io<T>::unpack(w[i]);
+            x[2 * i] = f.x;
+            x[2 * i + 1] = f.y;
+        }
+        if (a.pos) {
+            float ss = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
+#pragma unroll
+            for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffu << (threadIdx.x & 24), ss, o);
+            const float r = rsqrtf(ss * (1.0f / D) + a.eps);
+            if (on) {
+#pragma unroll
+                for (int i = 0; i < 8; ++i) x[i] = x[i] * r * gain[i];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int p = 4 * e + i;
+                    if (p < 3 * P) {
+                        const float2 cs = turn[tok][p];
+                        const float y0 = x[2 * i], y1 = x[2 * i + 1];
+                        x[2 * i] = y0 * cs.x - y1 * cs.y;
+                        x[2 * i + 1] = y0 * cs.y + y1 * cs.x;
+                    }
+                }
+            }
+        }
+        if (on)
+            *reinterpret_cast<uint4 *>(a.k_pages + (((page * a.hkv + head) * C + e) * kPage + slot + tok) * 8) =
+                make_uint4(sm100::pack_f16x2(x[0], x[1]), sm100::pack_f16x2(x[2], x[3]),
+                           sm100::pack_f16x2(x[4], x[5]), sm100::pack_f16x2(x[6], x[7]));
+    }
+
+    // values: a thread turns eight tokens x two channels
+    const uint32_t *v = static_cast<const uint32_t *>(a.v);
+    uint16_t *vp = static_cast<uint16_t *>(a.v_pages);
+    const int g0 = slot / 8, groups = (slot + t.count - 1) / 8 - g0 + 1;
+    for (int u = threadIdx.x; u < groups * a.hkv * (D / 2); u += kWriteThreads) {
+        const int p = u % (D / 2), head = u / (D / 2) % a.hkv, grp = g0 + u / (D / 2) / a.hkv;
+        uint32_t w[8];
+        const int tok0 = grp * 8 - slot;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int tok = tok0 + i;
+            w[i] = tok >= 0 && tok < t.count ? __ldg(v + ((t.row + tok) * a.hkv + head) * (D / 2) + p) : 0u;
+        }
+        uint16_t *dst = vp + (((page * a.hkv + head) * 16 + grp) * D + 2 * p) * 8;
+        if (tok0 >= 0 && tok0 + 8 <= t.count) {
+            uint32_t lo[4], hi[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                lo[i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x5410);
+                hi[i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);
+            }
+            reinterpret_cast<uint4 *>(dst)[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+            reinterpret_cast<uint4 *>(dst)[1] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int tok = tok0 + i;
+                if (tok < 0 || tok >= t.count) continue;
+                dst[i] = (uint16_t)w[i];
+                dst[8 + i] = (uint16_t)(w[i] >> 16);
+            }
+        }
+    }
+}
+
+// ------------------------------------------------------------------ copying pages
+//
+// The page numbers travel as kernel arguments (at most 32,764 bytes of them), so the call
+// needs neither a device buffer nor a copy that would have to outlive it.  Bound by memory:
+// a block moves 16 KB of a page, four 16-byte loads in flight a thread.
+
+constexpr int kCopyThreads = 256;
+constexpr int kCopyUnits = 1024;  // 16-byte units a block
+
+struct CopyArgs {
+    uint4 *k_pages, *v_pages;
+    int64_t page_units, pool_units;
+    int parts;
+};
+template <int N>
+struct CopyPairs {
+    int2 p[N];
+};
+
+template <int N>
+__global__ void __launch_bounds__(kCopyThreads) paged_copy_kernel(const __grid_constant__ CopyArgs a,
+                                                                  const __grid_constant__ CopyPairs<N> pairs) {
+    const int2 p = pairs.p[blockIdx.x / a.parts];
+    uint4 *pool = (blockIdx.z ? a.v_pages : a.k_pages) + blockIdx.y * a.pool_units;
+    const uint4 *src = pool + p.x * a.page_units;
+    uint4 *dst = pool + p.y * a.page_units;
+    const int64_t u0 = (int64_t)(blockIdx.x % a.parts) * kCopyUnits + threadIdx.x;
+    uint4 x[kCopyUnits / kCopyThreads];
+#pragma unroll
+    for (int i = 0; i < kCopyUnits / kCopyThreads; ++i)
+        if (u0 + i * kCopyThreads < a.page_units) x[i] = __ldcs(src + u0 + i * kCopyThreads);
+#pragma unroll
+    for (int i = 0; i < kCopyUnits / kCopyThreads; ++i)
+        if (u0 + i * kCopyThreads < a.page_units) __stcs(dst + u0 + i * kCopyThreads, x[i]);
+}
+
+template <int N>
+int launch_copy(const CopyArgs &a, const PagedCache &c, const int32_t *pairs, int64_t n, cudaStream_t stream) {
+    CopyPairs<N> p;
+    std::memcpy(p.p, pairs, (size_t)n * sizeof(int2));
+    const dim3 grid((unsigned)(n * a.parts), (unsigned)c.layers, 2);
+    paged_copy_kernel<N><<<grid, kCopyThreads, 0, stream>>>(a, p);
+    return cudaGetLastError() == cudaSuccess ? BCA_OK : BCA_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ joining the pieces
+//
+// O = sum_p 2^(r_p - r) O_p / sum_p 2^(r_p - r) l_p with r the largest reference, over the
+// pieces p of an item, always in the order of the blocks that made them.  Block c joins the
+// item that share c begins and does not end.  Eight lanes a piece and row, four pieces of a
+// row at a time.
+
+constexpr int kJoinThreads = 512;
+constexpr int kJoinRows = 16;
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a) {
+    __shared__ PagedLocate sh;
+    PagedCursor cur;
+    uint64_t lo, hi, total;
+    const int c = blockIdx.x;
+    const bool found = paged_locate(a, c, true, sh, lo, hi, total, cur);
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // nothing is cut behind share c, or the item began in an earlier share
+    if (!found || cur.start == hi || cur.start < lo) return;
+    const uint64_t end = cur.end();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / 8, e = lane % 8;
+    for (int row = blockIdx.y * kJoinRows + warp; row < min((int)(blockIdx.y + 1) * kJoinRows, a.rows);
+         row += kJoinThreads / 32) {
+        const int64_t packed = cur.t * a.rows + row;
+        if (packed / a.group >= cur.s.n) continue;
+        float ref = -INFINITY, sum = 0.f, o[D / 8] = {};
+        for (int x0 = c; x0 < a.shares; x0 += 4) {
+            const int x = x0 + sub;
+            const uint64_t from = paged_share(total, a.shares, x), to = paged_share(total, a.shares, x + 1);
+            int32_t p0 = 0, p1 = 0;
+            if (x < a.shares && from < end && to > from) cur.pages(a, from, to, p0, p1);
+            if (p0 < p1) {
+                const float *part = paged_part(a, D, 2 * x + (x == c ? 1 : 0));
+                const float r = part[a.rows * D + row], l = part[a.rows * (D + 1) + row];
+                float y[D / 8];
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) y[i] = part[(size_t)row * D + e + 8 * i];
+                const float top = fmaxf(ref, r);
+                const float mul = top == -INFINITY ? 0.f : sm100::ex2(ref - top);
+                const float add = top == -INFINITY ? 0.f : sm100::ex2(r - top);
+                sum = sum * mul + l * add;
+#pragma unroll
+                for (int i = 0; i < D / 8; ++i) o[i] = o[i] * mul + y[i] * add;
+                ref = top;
+            }
+            if (paged_share(total, a.shares, min(x0 + 4, a.shares)) >= end) break;
+        }
+#pragma unroll
+        for (int s = 8; s < 32; s <<= 1) {
+            const float r = __shfl_xor_sync(0xffffffffu, ref, s), l = __shfl_xor_sync(0xffffffffu, sum, s);
+            const float top = fmaxf(ref, r);
+            const float mul = top == -INFINITY ? 0.f : sm100::ex2(ref - top);
+            const float add = top == -INFINITY ? 0.f : sm100::ex2(r - top);
+            sum = sum * mul + l * add;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) o[i] = o[i] * mul + __shfl_xor_sync(0xffffffffu, o[i], s) * add;
+            ref = top;
+        }
+        if (sub != 0) continue;
+        const bool none = ref == -INFINITY;
+        const float inv = none ? 0.f : 1.f / sum;
+        const int64_t token = cur.s.r0 + packed / a.group;
+        const int head = cur.g * a.group + (int)(packed % a.group);
+        const int64_t at = (token * a.hq + head) * D;
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i) {
+            const float y = none ? 0.f : o[i] * inv;
+            if (a.o_fp32) static_cast<float *>(a.o)[at + e + 8 * i] = y;
+            else static_cast<T *>(a.o)[at + e + 8 * i] = T(y);
+        }
+        if (a.lse && e == 0)
+            a.lse[head * a.nq + token] = none ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+    }
+}
+
+template <int D, typename T>
+int launch_join(const PagedArgs &a, cudaStream_t stream) {
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)a.shares, (unsigned)((a.rows + kJoinRows - 1) / kJoinRows));
+    cfg.blockDim = dim3(kJoinThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T>, a) == cudaSuccess ? BCA_OK : BCA_ERR_CUDA;
+}
+
+// ------------------------------------------------------------------ by head size and type
+
+template <typename F>
+int by_type(const PagedCache &c, F &&f) {
+    const bool f16 = (c.flags & BCA_PAGED_FP16) != 0;
+    switch (c.d) {
+        case 24: return f16 ? f(std::integral_constant<int, 24>{}, __half{}) : f(std::integral_constant<int, 24>{}, __nv_bfloat16{});
+        case 32: return f16 ? f(std::integral_constant<int, 32>{}, __half{}) : f(std::integral_constant<int, 32>{}, __nv_bfloat16{});
+        case 48: return f16 ? f(std::integral_constant<int, 48>{}, __half{}) : f(std::integral_constant<int, 48>{}, __nv_bfloat16{});
+        default: return BCA_ERR_UNSUPPORTED;
+    }
+}
+
+}  // namespace
+
+PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices) {
+    PagedShape s;
+    // packed rows of an average slice
+    const int64_t rows = nq * (c.hq / c.hkv) / std::max(slices, 1);
+    s.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    s.shares = kSMs;
+    return s;
+}
+
+size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices) {
+    const PagedShape s = paged_shape(c, nq, slices);
+    return (size_t)s.shares * 2 * s.rows * (c.d + 2) * sizeof(float);
+}
+
+int prepare_paged(const PagedCache &c) { return prepare_paged_rows(c); }
+
+int launch_paged_write(const PagedCache &c, const PagedWriteIO &io, cudaStream_t stream) {
+    WriteArgs a;
+    a.k = io.k;
+    a.v = io.v;
+    a.pos = io.pos;
+    a.k_gain = io.k_gain;
+    a.table = io.table;
+    a.off = io.off;
+    a.start = io.start;
+    a.k_pages = static_cast<__half *>(io.k_pages);
+    a.v_pages = io.v_pages;
+    a.status = c.d_status;
+    a.n = io.n;
+    a.pages = c.pages;
+    a.seqs = io.seqs;
+    a.width = io.width;
+    a.hkv = c.hkv;
+    a.eps = c.eps;
+    std::memcpy(a.turns, c.turns, sizeof(a.turns));
+    const int64_t blocks = io.n / kWriteTokens + 2 * (int64_t)io.seqs;
+    if (blocks > INT32_MAX) return BCA_ERR_TOO_LARGE;
+    return by_type(c, [&](auto d, auto t) {
+        paged_write_kernel<decltype(d)::value, decltype(t)><<<(unsigned)blocks, kWriteThreads, 0, stream>>>(a);
+        return cudaGetLastError() == cudaSuccess ? BCA_OK : BCA_ERR_CUDA;
+    });
+}
+
+int launch_paged_copy(const PagedCache &c, const int32_t *pairs, int64_t n, void *k_pages, void *v_pages,
+                      cudaStream_t stream) {
+    CopyArgs a;
+    a.k_pages = static_cast<uint4 *>(k_pages);
+    a.v_pages = static_cast<uint4 *>(v_pages);
+    a.page_units = (int64_t)c.hkv * c.d * kPage / 8;
+    a.pool_units = a.page_units * c.pages;
+    const int64_t parts = (a.page_units + kCopyUnits - 1) / kCopyUnits;
+    if (parts > INT32_MAX / 4000) return BCA_ERR_TOO_LARGE;
+    a.parts = (int)parts;
+    // A launch's arguments are copied whatever part of them is used, hence two sizes.
+    for (int64_t at = 0; at < n;) {
+        const int64_t m = std::min<int64_t>(n - at, n - at <= 480 ? 480 : 4000);
+        const int rc = m <= 480 ? launch_copy<480>(a, c, pairs + 2 * at, m, stream)
+                                : launch_copy<4000>(a, c, pairs + 2 * at, m, stream);
+        if (rc != BCA_OK) return rc;
+        at += m;
+    }
+    return BCA_OK;
+}
+
+int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream_t stream) {
+    const PagedShape s = paged_shape(c, io.nq, io.slices);
+    PagedArgs a;
+    a.q = io.q;
+    a.pos = io.pos;
+    a.q_gain = io.q_gain;
+    a.k_pages = io.k_pages;
+    a.v_pages = io.v_pages;
+    a.table = io.table;
+    a.off = io.off;
+    a.seq = io.seq;
+    a.k_begin = io.k_begin;
+    a.k_end = io.k_end;
+    a.o = io.o;
+    a.lse = io.lse;
+    a.part = static_cast<float *>(io.workspace);
+    a.status = c.d_status;
+    a.nq = io.nq;
+    a.pages = c.pages;
+    a.seqs = io.seqs;
+    a.width = io.width;
+    a.slices = io.slices;
+    a.causal = io.causal;
+    a.hq = c.hq;
+    a.hkv = c.hkv;
+    a.group = c.hq / c.hkv;
+    a.rows = s.rows;
+    a.shares = s.shares;
+    a.o_fp32 = (c.flags & BCA_O_FP32) ? 1 : 0;
+    a.eps = c.eps;
+    a.scale = 1.4426950408889634f / std::sqrt((float)c.d);
+    a.timeout_ns = (c.flags & BCA_TEST_FORCE_TIMEOUT) ? 1000000ull : kPagedWaitNs;
+    a.skip_loads = (c.flags & BCA_TEST_FORCE_TIMEOUT) ? 1 : 0;
+    std::memcpy(a.turns, c.turns, sizeof(a.turns));
+    // the row of items must stay below 2^62 long (rows of q and tables this large do not fit a GPU)
+    const double tiles = (double)io.nq * a.group / a.rows + io.slices;
+    if (tiles * c.hkv * ((double)io.width * kPage + (double)io.nq + kItemWeight) > 4e18) return BCA_ERR_TOO_LARGE;
+    const int rc = launch_paged_rows(c, a, stream);
+    if (rc != BCA_OK) return rc;
+    return by_type(c, [&](auto d, auto t) { return launch_join<decltype(d)::value, decltype(t)>(a, stream); });
+}
+
+}  // namespace bca

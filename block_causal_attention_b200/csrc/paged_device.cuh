@@ -1,0 +1,348 @@
+// Device code shared by the paged-cache kernels: a call's arguments, how its work is cut
+// into equal shares, and the QK-Norm + 3D RoPE of rows at explicit positions.
+#pragma once
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cstdint>
+
+#include "paged.hpp"
+#include "prologue.cuh"
+#include "sm100.cuh"
+
+namespace bca {
+
+struct PagedArgs {
+    const void *q;
+    const int32_t *pos;   // [nq][3], or null: q given post-prologue
+    const float *q_gain;
+    const void *k_pages, *v_pages;
+    const int32_t *table;
+    const int32_t *off, *seq, *k_begin, *k_end;  // seq null: slice i reads row i
+    void *o;
+    float *lse;
+    // parts of items that several blocks share: slot 2c (block c goes on with an item) and
+    // 2c + 1 (it begins one that it does not end); a slot is [rows][D] O, [rows] reference,
+    // [rows] sum, fp32
+    float *part;
+    int *status;
+    int64_t nq, pages;
+    int seqs, width, slices, causal;
+    int hq, hkv, group;
+    int rows;             // packed rows of a tile
+    int shares;           // blocks of the attention kernel
+    int o_fp32;
+    float eps;
+    float scale;          // log2(e) / sqrt(D)
+    uint64_t timeout_ns;
+    int skip_loads;       // failure-detection test: issue no page loads
+    double turns[24];
+};
+
+// ------------------------------------------------------------------ the work and its shares
+//
+// A slice's queries are packed token by token, the `group` query heads of a KV head next to
+// one another, and cut into tiles of `rows` packed rows: the rows of a tile read the same
+// keys.  An item is a tile of one KV head.  Items stand in a row (slice, KV head, tile), each
+// as long as its weight, about the keys it reads; block c takes the c-th of `shares` equal
+// stretches of that row.  A stretch that ends inside an item splits the item's pages in
+// proportion; the pieces are joined by paged_join_kernel.  So the load is even whatever the
+// lengths are (they are device data), and the cut depends on the arguments alone: the same
+// call gives the same bits.
+
+// Weight of an item that reads no page, in keys: its prologue, its epilogue and the start
+// of its loads.
+constexpr int64_t kItemWeight = 128;
+
+struct PagedSlice {
+    int32_t r0, n;        // its rows of q
+    int32_t b;            // table row
+    int32_t kb, ke;       // keys [kb, ke) that it sees; kb == ke: none
+    int32_t end;          // k_end as given (>= 0): the causal rule counts back from it
+    int64_t tiles;        // of one KV head
+    int64_t w0, dw;       // weight of tile t: w0 + dw * (t + 1)
+
+    __device__ __forceinline__ uint64_t upto(int64_t t) const {  // weight of its first t tiles
+        return (uint64_t)(t * w0 + dw * (t * (t + 1) / 2));
+    }
+    __device__ __forceinline__ uint64_t weight(int64_t t) const { return (uint64_t)(w0 + dw * (t + 1)); }
+};
+
+__device__ __forceinline__ PagedSlice paged_slice(const PagedArgs &a, int i) {
+    PagedSlice s;
+    const int32_t nq = (int32_t)a.nq;
+    const int32_t o0 = __ldg(a.off + i), o1 = __ldg(a.off + i + 1);
+    const int32_t b = a.seq ? __ldg(a.seq + i) : i, kb = __ldg(a.k_begin + i), ke = __ldg(a.k_end + i);
+    s.r0 = min(max(o0, 0), nq);
+    s.n = min(max(o1, s.r0), nq) - s.r0;
+    s.b = b;
+    s.end = max(ke, 0);
+    s.kb = max(kb, 0);
+    s.ke = min(s.end, a.width * kPage);
+    if (b < 0 || b >= a.seqs || s.ke <= s.kb) s.kb = s.ke = 0;
+    s.tiles = ((int64_t)s.n * a.group + a.rows - 1) / a.rows;
+    const int64_t keys = s.ke - s.kb;
+    if (a.causal) {
+        s.dw = a.rows / a.group;
+        s.w0 = kItemWeight + max(keys - s.n, (int64_t)0);
+    } else {
+        s.dw = 0;
+        s.w0 = kItemWeight + keys;
+    }
+    return s;
+}
+
+// First key that row `token` (counted in the slice) does not see.
+__device__ __forceinline__ int32_t paged_limit(const PagedArgs &a, const PagedSlice &s, int32_t token) {
+    if (!a.causal) return s.ke;
+    return min(s.ke, s.end - (s.n - 1 - token));  // no overflow: both are >= 0 and below 2^31
+}
+
+// Where share c begins in a row of this total weight.
+__device__ __forceinline__ uint64_t paged_share(uint64_t total, int shares, int c) {
+    return total / shares * c + total % shares * c / shares;
+}
+
+struct PagedCursor {
+    PagedSlice s;
+    int32_t slice;
+    int32_t g;          // KV head
+    int64_t t;          // tile
+    uint64_t start;     // where the item begins
+
+    __device__ __forceinline__ uint64_t end() const { return start + s.weight(t); }
+
+    // Pages of the item, and the part of them that lies in [lo, hi).
+    __device__ __forceinline__ void pages(const PagedArgs &a, uint64_t lo, uint64_t hi, int32_t &p0,
+                                          int32_t &p1) const {
+        const int64_t last = min(((t + 1) * a.rows - 1) / a.group, (int64_t)s.n - 1);
+        const int32_t ke = paged_limit(a, s, (int32_t)last);
+        const int32_t first = s.kb / kPage;
+        const uint64_t np = ke > s.kb ? (uint64_t)((ke - 1) / kPage + 1 - first) : 0;
+        const uint64_t w = s.weight(t);
+        p0 = first + (lo > start ? (int32_t)(np * (lo - start) / w) : 0);
+        p1 = first + (int32_t)(hi < start + w ? np * (hi - start) / w : np);
+    }
+
+    // The next item (all 32 lanes of a warp together: slices without rows are passed over 32
+    // at a time).  False behind the last one.
+    __device__ __forceinline__ bool next(const PagedArgs &a) {
+        start = end();
+        if (++t < s.tiles) return true;
+        t = 0;
+        if (++g < a.hkv) return true;
+        g = 0;
+        for (int base = slice + 1; base < a.slices; base += 32) {
+            const int i = base + (int)(threadIdx.x & 31);
+            bool some = false;
+            if (i < a.slices) {
+                const int32_t nq = (int32_t)a.nq;
+                const int32_t r0 = min(max(__ldg(a.off + i), 0), nq);
+                some = min(max(__ldg(a.off + i + 1), r0), nq) > r0;
+            }
+            const uint32_t m = __ballot_sync(0xffffffffu, some);
+            if (m) {
+                slice = base + __ffs(m) - 1;
+                s = paged_slice(a, slice);
+                return true;
+            }
+        }
+        return false;
+    }
+};
+
+struct PagedLocate {
+    uint64_t warp_sum[32];
+    uint64_t pre;
+    int32_t slice;
+};
+
+// The item that share c begins in (`at_end` = false), or that the cut behind it lies in.
+// All threads of the block together (a multiple of 32, at most 1024).  lo, hi: the stretch.
+// False, for the whole block, when there is none.
+__device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, bool at_end, PagedLocate &sh, uint64_t &lo,
+                                             uint64_t &hi, uint64_t &total, PagedCursor &cur) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
+    uint64_t mine = 0, sum = 0;
+    for (int i = tid; i < a.slices; i += blockDim.x) {
+        const PagedSlice s = paged_slice(a, i);
+        mine = a.hkv * s.upto(s.tiles);
+        sum += mine;
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) sh.warp_sum[warp] = sum;
+    if (tid == 0) sh.slice = -1;
+    __syncthreads();
+    total = 0;
+    for (int w = 0; w < warps; ++w) total += sh.warp_sum[w];
+    lo = paged_share(total, a.shares, c);
+    hi = paged_share(total, a.shares, c + 1);
+    const uint64_t target = at_end ? hi : lo;
+    if (target >= total || (!at_end && lo == hi)) return false;
+
+    uint64_t carry = 0;
+    for (int base = 0; base < a.slices; base += blockDim.x) {
+        const int i = base + tid;
+        if (a.slices > (int)blockDim.x) {
+            mine = 0;
+            if (i < a.slices) {
+                const PagedSlice s = paged_slice(a, i);
+                mine = a.hkv * s.upto(s.tiles);
+            }
+        }
+        uint64_t inc = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const uint64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += v;
+        }
+        __syncthreads();
+        if (lane == 31) sh.warp_sum[warp] = inc;
+        __syncthreads();
+        uint64_t before = carry, block = 0;
+        for (int w = 0; w < warps; ++w) {
+            if (w < warp) before += sh.warp_sum[w];
+            block += sh.warp_sum[w];
+        }
+        const uint64_t pre = before + inc - mine;
+        if (pre <= target && target - pre < mine) {
+            sh.slice = i;
+            sh.pre = pre;
+        }
+        carry += block;
+        if (carry > target) break;
+    }
+    __syncthreads();
+    cur.slice = sh.slice;
+    if (cur.slice < 0) return false;
+    cur.s = paged_slice(a, cur.slice);
+    const uint64_t per_head = cur.s.upto(cur.s.tiles);
+    uint64_t rest = target - sh.pre;
+    cur.g = (int32_t)(rest / per_head);
+    rest %= per_head;
+    int64_t t;
+    if (cur.s.dw == 0) {
+        t = (int64_t)(rest / (uint64_t)cur.s.w0);
+    } else {
+        // upto(t) <= rest, a quadratic in t; the loops take the rounding out
+        const double h = (double)cur.s.w0 + 0.5 * cur.s.dw;
+        t = (int64_t)((sqrt(h * h + 2.0 * cur.s.dw * (double)rest) - h) / cur.s.dw);
+    }
+    t = min(max(t, (int64_t)0), cur.s.tiles - 1);
+    while (t > 0 && cur.s.upto(t) > rest) --t;
+    while (t + 1 < cur.s.tiles && cur.s.upto(t + 1) <= rest) ++t;
+    cur.t = t;
+    cur.start = target - (rest - cur.s.upto(t));
+    return true;
+}
+
+__device__ __forceinline__ float *paged_part(const PagedArgs &a, int d, int slot) {
+    return a.part + (size_t)slot * a.rows * (d + 2);
+}
+
+// ------------------------------------------------------------------ types
+
+template <typename T>
+struct Io;
+template <>
+struct Io<__nv_bfloat16> {
+    static constexpr bool kF16 = false;
+    // P = 2^(s - reference) in bf16 has fp32's exponents: no shift is needed
+    static constexpr float kShift = 0.f;
+    static __device__ __forceinline__ float2 unpack(uint32_t u) {
+        return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u));
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return sm100::pack_bf16x2(lo, hi); }
+    static __device__ __forceinline__ bool bad(uint32_t bits) { return (bits & 0x7f80u) == 0x7f80u; }
+};
+template <>
+struct Io<__half> {
+    static constexpr bool kF16 = true;
+    // The reference is put 6 below the running maximum: P then lies between 2^-24 (fp16's
+    // smallest) and 2^6, up to 2^14 before the reference moves, below fp16's 65504; without
+    // it a key 2^-14 below the largest would already lose bits of its P.
+    static constexpr float kShift = 6.f;
+    static __device__ __forceinline__ float2 unpack(uint32_t u) {
+        return __half22float2(*reinterpret_cast<const __half2 *>(&u));
+    }
+    static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return sm100::pack_f16x2(lo, hi); }
+    static __device__ __forceinline__ bool bad(uint32_t bits) { return (bits & 0x7c00u) == 0x7c00u; }
+};
+
+// The reference moves when a score passes it by more than this (in powers of two).
+constexpr float kLazy = 8.f;
+
+// ------------------------------------------------------------------ rows at explicit positions
+
+// cos and sin of position * base^(-i/P): the turns in 64 bits, so that far positions keep
+// their angle (in fp32 position 10^6 would be off by 0.06 rad), less the whole ones, in fp32.
+__device__ __forceinline__ float2 paged_cos_sin(int32_t position, double turns) {
+    const double x = position * turns;
+    const float f = (float)(x - rint(x));
+    float2 cs;
+    sincospif(2.f * f, &cs.y, &cs.x);
+    return cs;
+}
+
+// What eight lanes make of a row: lane e has channel pairs e, e + 8, e + 16 (those below
+// D / 2).  x: the raw values in, QK-Norm and RoPE applied out.
+template <int D>
+struct Row8 {
+    static constexpr int P = Geo<D>::PAIRS;
+    static constexpr int N = (D / 2 + 7) / 8;
+    float2 x[N];
+
+    template <typename T>
+    __device__ __forceinline__ void load(const T *row, int e) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = e + 8 * i;
+            x[i] = p < D / 2 ? Io<T>::unpack(__ldg(reinterpret_cast<const uint32_t *>(row) + p)) : float2{0.f, 0.f};
+        }
+    }
+
+    __device__ __forceinline__ void prologue(const int32_t *pos, const float *gain, const double *turns, float eps,
+                                             int e) {
+        float ss = 0.f;
+#pragma unroll
+        for (int i = 0; i < N; ++i) ss = fmaf(x[i].x, x[i].x, fmaf(x[i].y, x[i].y, ss));
+#pragma unroll
+        for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
+        const float r = rsqrtf(ss * (1.0f / D) + eps);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = e + 8 * i;
+            if (p >= D / 2) continue;
+            float y0 = x[i].x * r, y1 = x[i].y * r;
+            if (gain) {
+                y0 *= __ldg(gain + 2 * p);
+                y1 *= __ldg(gain + 2 * p + 1);
+            }
+            if (p < 3 * P) {
+                const int axis = p / P;
+                const float2 cs = paged_cos_sin(__ldg(pos + axis), turns[8 * axis + p - axis * P]);
+                x[i] = make_float2(y0 * cs.x - y1 * cs.y, y0 * cs.y + y1 * cs.x);
+            } else {
+                x[i] = make_float2(y0, y1);
+            }
+        }
+    }
+};
+
+// ------------------------------------------------------------------ bounded waits
+
+constexpr uint64_t kPagedWaitNs = 2000000000ull;  // a healthy wait is microseconds
+
+__device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, const PagedArgs &a,
+                                           volatile int *abort_flag) {
+    if (sm100::mbar_try_wait(bar, parity)) return true;
+    if (*abort_flag) return false;
+    if (sm100::mbar_wait(bar, parity, a.timeout_ns)) return true;
+    atomicOr(a.status, kPagedTimeout);
+    *abort_flag = 1;
+    return false;
+}
+
+}  // namespace bca

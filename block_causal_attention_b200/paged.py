@@ -1,0 +1,340 @@
+"""The KV cache in pages: device operators (``PagedCache``) and page bookkeeping (``PagePool``).
+
+A contiguous KV cache belongs to one video and is re-packed whenever its window slides.  In
+pages of 128 tokens keys and values are written once and stay; several videos of any lengths
+share one pool and one call; a fork shares its parent's pages until it writes (MAGI-1 research
+notes, "Inference tricks > KV Cache": the cache of earlier chunks and its range).  The layouts
+and the rules are in include/bca.h, "paged KV cache".
+"""
+from __future__ import annotations
+
+import heapq
+from typing import Dict, List, Optional, Sequence
+
+import numpy as np
+
+from . import _abi
+
+PAGE = _abi.BCA_PAGE_TOKENS
+
+
+class PagedCache:
+    """A pool of pages for `layers` layers and the operators on it: ``write`` new tokens,
+    ``copy_pages`` and ``attend``.
+
+    `dtype` (bf16 or fp16) is the type of q, k, v, o and the stored values; stored keys are
+    fp16, post-prologue.  `k_pages` / `v_pages` may be given (contiguous CUDA tensors of
+    ``k_shape`` / ``v_shape``); otherwise they are allocated, uninitialised."""
+
+    def __init__(self, hq: int, hkv: int, d: int, pages: int, *, layers: int = 1, dtype=None,
+                 rope_base=(1e4, 1e4, 1e4), eps: float = 1e-6, o_fp32: bool = False, k_pages=None, v_pages=None,
+                 host_only: bool = False, test_force_timeout: bool = False):
+        import torch
+        dtype = torch.bfloat16 if dtype is None else dtype
+        if dtype not in (torch.bfloat16, torch.float16):
+            raise ValueError(f"dtype: expected torch.bfloat16 or torch.float16, got {dtype}")
+        desc = _abi.bca_paged_desc()
+        desc.num_q_heads, desc.num_kv_heads, desc.head_dim = int(hq), int(hkv), int(d)
+        desc.num_layers, desc.num_pages = int(layers), int(pages)
+        desc.rope_base[:] = [float(x) for x in rope_base]
+        desc.norm_eps = float(eps)
+        desc.flags = (_abi.BCA_PAGED_FP16 if dtype == torch.float16 else 0) | (_abi.BCA_O_FP32 if o_fp32 else 0) | \
+            (_abi.BCA_PLAN_HOST_ONLY if host_only else 0) | \
+            (_abi.BCA_TEST_FORCE_TIMEOUT if test_force_timeout else 0)
+        self._lib = _abi.lib()
+        self._h = _abi.ctypes.c_void_p()
+        _abi.check(self._lib.bca_paged_create(_abi.ctypes.byref(desc), _abi.ctypes.byref(self._h)),
+                   "bca_paged_create")
+        self.hq, self.hkv, self.d, self.pages, self.layers = int(hq), int(hkv), int(d), int(pages), int(layers)
+        self.dtype, self.o_fp32, self.host_only = dtype, bool(o_fp32), bool(host_only)
+        self.k_shape = (self.layers, self.pages, self.hkv, self.d // 8, PAGE, 8)
+        self.v_shape = (self.layers, self.pages, self.hkv, PAGE // 8, self.d, 8)
+        self.pool_bytes = int(self._lib.bca_paged_pool_bytes(self._h))
+        self.k_pages = self.v_pages = self.device = None
+        if self.host_only:
+            return
+        self.device = torch.device("cuda", torch.cuda.current_device())
+        for name, t, dt, shape in (("k_pages", k_pages, torch.float16, self.k_shape),
+                                   ("v_pages", v_pages, dtype, self.v_shape)):
+            if t is None:
+                t = torch.empty(shape, dtype=dt, device=self.device)
+            else:
+                self._tensor(name, t, dt, shape)
+            setattr(self, name, t)
+
+    # ------------------------------------------------------------------ arguments
+    def _tensor(self, name, t, dtype, shape):
+        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
+            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {self.device}, got "
+                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
+        return t.data_ptr()
+
+    def _prologue(self, rows, pos, gain, gain_name):
+        import torch
+        if pos is None and gain is not None:
+            raise ValueError(f"{gain_name} needs pos: rows without positions are taken as post-prologue")
+        return (None if pos is None else self._tensor("pos", pos, torch.int32, (rows, 3)),
+                None if gain is None else self._tensor(gain_name, gain, torch.float32, (self.d,)))
+
+    def _layer(self, layer):
+        if self.host_only:
+            raise _abi.BcaError(_abi.BCA_ERR_HOST_ONLY_PLAN, "paged cache")
+        if not 0 <= layer < self.layers:
+            raise ValueError(f"layer {layer} of {self.layers}")
+        at = layer * self.pool_bytes
+        return self.k_pages.data_ptr() + at, self.v_pages.data_ptr() + at
+
+    def _table(self, table):
+        import torch
+        if table.dim() != 2:
+            raise ValueError("table: expected int32 [seqs, width]")
+        return self._tensor("table", table, torch.int32, tuple(table.shape)), table.shape[0], table.shape[1]
+
+    def _stream(self, stream):
+        import torch
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else stream
+
+    # ------------------------------------------------------------------ operators
+    def write(self, k, v, table, off, start, *, pos=None, k_gain=None, layer: int = 0, stream=None) -> None:
+        """Put rows off[b] .. off[b + 1] - 1 of k and v [n, Hkv, D] into the pages of table row
+        b as its tokens start[b], start[b] + 1, ...  With pos (int32 [n, 3]) the keys pass
+        through QK-Norm (k_gain, or ones) and RoPE; without, they are given post-prologue.
+        table, off, start, pos: int32 tensors on the cache's device, read when the kernel runs.
+        A token that has no page is dropped and reported by ``status``."""
+        import torch
+        kp, vp = self._layer(layer)
+        n = k.shape[0]
+        shape = (n, self.hkv, self.d)
+        kq, vq = self._tensor("k", k, self.dtype, shape), self._tensor("v", v, self.dtype, shape)
+        tab, seqs, width = self._table(table)
+        o = self._tensor("off", off, torch.int32, (seqs + 1,))
+        s = self._tensor("start", start, torch.int32, (seqs,))
+        p, gain = self._prologue(n, pos, k_gain, "k_gain")
+        rc = self._lib.bca_paged_write(self._h, kq, vq, n, p, gain, tab, seqs, width, o, s, kp, vp,
+                                       self._stream(stream))
+        if rc:
+            _abi.check(rc, "bca_paged_write")
+
+    def copy_pages(self, pairs, *, stream=None) -> None:
+        """Make page pairs[i, 1] a copy of page pairs[i, 0], in every layer.  pairs: [n, 2] on
+        the host (a CPU tensor, an array or a list), read before the call returns.  A page may
+        be written once, and none that is written may be read."""
+        if hasattr(pairs, "is_cuda") and pairs.is_cuda:
+            raise ValueError("pairs: expected host data")
+        pairs = np.asarray(pairs)
+        if pairs.size and (pairs.ndim != 2 or pairs.shape[1] != 2 or pairs.dtype.kind not in "iu"):
+            raise ValueError(f"pairs: expected whole numbers [n, 2], got {pairs.dtype} {pairs.shape}")
+        if pairs.dtype != np.int32:
+            if pairs.size and (pairs.min() < 0 or pairs.max() >= self.pages):
+                raise _abi.BcaError(_abi.BCA_ERR_BAD_PAGE, "bca_paged_copy")
+            pairs = pairs.astype(np.int32)
+        pairs = np.ascontiguousarray(pairs)
+        kp, vp = self._layer(0)
+        rc = self._lib.bca_paged_copy(self._h, pairs.ctypes.data, len(pairs), kp, vp, self._stream(stream))
+        if rc:
+            _abi.check(rc, "bca_paged_copy")
+
+    def attend(self, q, table, off, k_begin, k_end, *, seq=None, causal: bool = False, pos=None, q_gain=None,
+               layer: int = 0, o=None, lse=None, workspace=None, stream=None):
+        """Attention of q [nq, Hq, D] over the pages.  Rows off[i] .. off[i + 1] - 1 are slice i
+        and see tokens k_begin[i] .. k_end[i] - 1 of table row seq[i] (seq=None: slice i reads
+        row i), all of them, or with causal=True aligned at the last row and key.  pos (int32
+        [nq, 3]) and q_gain as in ``write``.  off, seq, k_begin, k_end and table are int32
+        tensors on the cache's device, read when the kernel runs.
+
+        Returns o; rows that see no key are zero.  Rows outside every slice are left as they
+        were in a given o (else uninitialised).  lse (fp32 [Hq, nq], optional) is filled in."""
+        import torch
+        kp, vp = self._layer(layer)
+        nq = q.shape[0]
+        qp = self._tensor("q", q, self.dtype, (nq, self.hq, self.d))
+        tab, seqs, width = self._table(table)
+        slices = off.shape[0] - 1 if off.dim() == 1 else -1
+        if slices < 0:
+            raise ValueError("off: expected int32 [slices + 1]")
+        i32, per_slice = torch.int32, (slices,)
+        offp = self._tensor("off", off, i32, (slices + 1,))
+        if seq is None and slices != seqs:
+            raise ValueError("seq=None needs as many slices as table rows")
+        sp = None if seq is None else self._tensor("seq", seq, i32, per_slice)
+        kb = self._tensor("k_begin", k_begin, i32, per_slice)
+        ke = self._tensor("k_end", k_end, i32, per_slice)
+        p, gain = self._prologue(nq, pos, q_gain, "q_gain")
+        odt = torch.float32 if self.o_fp32 else self.dtype
+        if o is None:
+            o = torch.empty((nq, self.hq, self.d), dtype=odt, device=self.device)
+        op = self._tensor("o", o, odt, (nq, self.hq, self.d))
+        lp = None if lse is None else self._tensor("lse", lse, torch.float32, (self.hq, nq))
+        if workspace is None:
+            workspace = self.alloc_workspace(nq, slices, stream)
+        elif workspace.numel() * workspace.element_size() < self.workspace_bytes(nq, slices) or \
+                workspace.device != self.device or not workspace.is_contiguous():
+            raise ValueError(f"workspace: expected {self.workspace_bytes(nq, slices)} contiguous bytes on {self.device}")
+        rc = self._lib.bca_paged_attend(self._h, qp, nq, p, gain, kp, vp, tab, seqs, width, offp, sp, kb, ke, slices,
+                                        1 if causal else 0, op, lp, workspace.data_ptr(), self._stream(stream))
+        if rc:
+            _abi.check(rc, "bca_paged_attend")
+        return o
+
+    def workspace_bytes(self, nq: int, slices: int) -> int:
+        return int(self._lib.bca_paged_workspace_bytes(self._h, nq, slices))
+
+    def alloc_workspace(self, nq: int, slices: int, stream=None):
+        """Workspace of an ``attend`` call of these sizes, on its stream.  Calls that may overlap
+        on the GPU (two streams, two captured graphs replayed side by side) need one each."""
+        import torch
+        n = max(16, self.workspace_bytes(nq, slices))
+        if stream is None:
+            return torch.empty(n, dtype=torch.uint8, device=self.device)
+        if not hasattr(stream, "cuda_stream"):
+            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
+        with torch.cuda.stream(stream):   # so that its next user is behind this call
+            return torch.empty(n, dtype=torch.uint8, device=self.device)
+
+    def status(self, stream=None) -> int:
+        """Status of the work on `stream`, waited for: BCA_OK, BCA_ERR_DEVICE_TIMEOUT, or
+        BCA_ERR_BAD_PAGE when a written token had no page.  Reading it clears it."""
+        return int(self._lib.bca_paged_status(self._h, None if self.host_only else self._stream(stream)))
+
+    def close(self) -> None:
+        if getattr(self, "_h", None) is not None and self._h.value:
+            self._lib.bca_paged_destroy(self._h)
+            self._h = _abi.ctypes.c_void_p()
+
+    def __enter__(self) -> "PagedCache":
+        return self
+
+    def __exit__(self, *exc) -> None:
+        self.close()
+
+    def __del__(self):
+        try:
+            self.close()
+        except Exception:
+            pass
+
+
+class PagePool:
+    """Which page belongs to whom: sequences with page tables, shared pages counted, pages
+    copied before a write when they are shared.  Host bookkeeping only; the copies it asks for
+    (lists of (from, to)) go to ``PagedCache.copy_pages``."""
+
+    def __init__(self, pages: int):
+        if pages < 1:
+            raise ValueError("pages >= 1 is required")
+        self.pages = int(pages)
+        self._free = list(range(self.pages))       # a heap: the lowest free page first
+        self._users = np.zeros(self.pages, np.int64)
+        self._rows: Dict[int, List[int]] = {}      # pages in order; -1: released
+        self._next = 0
+
+    @property
+    def free_pages(self) -> int:
+        return len(self._free)
+
+    def open(self) -> int:
+        """A new, empty sequence."""
+        self._next += 1
+        self._rows[self._next] = []
+        return self._next
+
+    def _row(self, seq: int) -> List[int]:
+        if seq not in self._rows:
+            raise KeyError(f"no open sequence {seq}")
+        return self._rows[seq]
+
+    def row(self, seq: int) -> List[int]:
+        """The sequence's pages in order (-1: released)."""
+        return list(self._row(seq))
+
+    def _release(self, page: int) -> None:
+        if page >= 0:
+            self._users[page] -= 1
+            if self._users[page] == 0:
+                heapq.heappush(self._free, page)
+
+    def _take(self) -> int:
+        page = heapq.heappop(self._free)
+        self._users[page] = 1
+        return page
+
+    def grow(self, seq: int, begin: int, end: int) -> List[tuple]:
+        """Make tokens [begin, end) of the sequence writable: pages up to `end` exist (released
+        ones in that stretch come back, empty), and those that [begin, end) touches are its
+        own.  Returns the page copies to make before the write.  Raises MemoryError, with
+        nothing changed, when the pool has too few free pages."""
+        if begin < 0 or end < begin:
+            raise ValueError(f"tokens [{begin}, {end})")
+        row = self._row(seq)
+        if begin == end:
+            return []
+        first, last = begin // PAGE, (end + PAGE - 1) // PAGE
+        touched = range(first, min(last, len(row)))
+        need = max(0, last - len(row)) + sum(1 for i in touched if row[i] < 0 or self._users[row[i]] > 1)
+        if need > len(self._free):
+            raise MemoryError(f"{need} pages needed, {len(self._free)} free")
+        moves = []
+        for i in touched:
+            old = row[i]
+            if old < 0:
+                row[i] = self._take()
+            elif self._users[old] > 1:
+                row[i] = self._take()
+                self._users[old] -= 1
+                if i * PAGE < begin or (i + 1) * PAGE > end:   # else every slot is written anew
+                    moves.append((old, row[i]))
+        while len(row) < last:
+            row.append(self._take())
+        return moves
+
+    def fork(self, seq: int) -> int:
+        """A new sequence with the same tokens, sharing every page."""
+        row = list(self._row(seq))
+        for p in row:
+            if p >= 0:
+                self._users[p] += 1
+        new = self.open()
+        self._rows[new] = row
+        return new
+
+    def release_before(self, seq: int, token: int) -> None:
+        """Give back the pages that hold only tokens before `token` (behind a KV range)."""
+        row = self._row(seq)
+        for i in range(min(max(token, 0) // PAGE, len(row))):
+            self._release(row[i])
+            row[i] = -1
+
+    def close(self, seq: int) -> None:
+        """End a sequence and give its pages back."""
+        for p in self._row(seq):
+            self._release(p)
+        del self._rows[seq]
+
+    def compact(self) -> List[tuple]:
+        """Move the pages in use to the front of the pool.  Returns the copies to make; the
+        tables already hold the new numbers."""
+        used = int(np.count_nonzero(self._users))
+        holes = [p for p in range(used) if self._users[p] == 0]
+        high = [p for p in range(used, self.pages) if self._users[p] > 0]
+        new = dict(zip(high, holes))
+        for a, b in new.items():
+            self._users[b], self._users[a] = self._users[a], 0
+        for row in self._rows.values():
+            row[:] = [new.get(p, p) for p in row]
+        self._free = [p for p in range(self.pages) if self._users[p] == 0]
+        heapq.heapify(self._free)
+        return list(new.items())
+
+    def table(self, seqs: Sequence[int], width: Optional[int] = None) -> np.ndarray:
+        """int32 [len(seqs), width] (width: the longest row's, or given), absent pages -1."""
+        rows = [self._row(s) for s in seqs]
+        need = max((len(r) for r in rows), default=0)
+        width = need if width is None else width
+        if width < need:
+            raise ValueError(f"width {width}: the longest row has {need} pages")
+        out = np.full((len(rows), width), -1, np.int32)
+        for i, r in enumerate(rows):
+            out[i, :len(r)] = r
+        return out

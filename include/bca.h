@@ -64,6 +64,7 @@ extern "C" {
 #define BCA_ERR_HOST_ONLY_PLAN (-7)    /* plan was built with BCA_PLAN_HOST_ONLY */
 #define BCA_ERR_NO_MEMORY (-8)         /* host or device allocation failed in bca_plan_create */
 #define BCA_ERR_TOO_LARGE (-9)         /* problem needs more scratch than the static workspace holds */
+#define BCA_ERR_BAD_PAGE (-10)         /* a new token had no page to go to, or a page move is not allowed */
 
 /* AttnSlice type */
 #define BCA_SLICE_FULL 0
@@ -331,6 +332,106 @@ int bca_profile_read(bca_plan_t plan, int kernel, int64_t *launches, double *tot
 /* Device status word of the plan (timeouts recorded by its kernels).  Synchronises
  * the stream, returns BCA_OK or the recorded error, and clears it. */
 int bca_status(bca_plan_t plan, void *stream);
+
+/* ------------------------------------------------------------------ paged KV cache
+ *
+ * The KV cache of earlier chunks (MAGI-1 research notes, "Inference tricks > KV Cache")
+ * in pages of BCA_PAGE_TOKENS tokens, for programs that serve several videos at a time or
+ * slide one for long: keys and values are written once, where they stay, sequences can
+ * share pages, and the masks, lengths and tables of a call are device data, so that a
+ * captured CUDA graph serves every step.  A page holds its tokens in the tile layout that
+ * the attention kernels' matrix instructions read, so no call re-lays the cache out:
+ *
+ *   k_pages [pages][Hkv][D/8][128][8]  fp16: channel c of token s at [c/8][s][c%8]; keys are
+ *                                      post-prologue (QK-Norm and RoPE applied), |x| < 65504
+ *   v_pages [pages][Hkv][16][D][8]     io type (bf16, or fp16 with BCA_PAGED_FP16): channel c
+ *                                      of token s at [s/8][c][s%8]
+ *
+ * One pool holds the pages of one layer; a cache of L layers is L pools back to back.
+ *
+ *   table [seqs][width] int32: row b lists sequence b's pages in order; its token p lies in
+ *   page table[b][p / 128] at slot p % 128.  An entry outside [0, num_pages) is an absent
+ *   page: it holds no keys (pages freed behind a KV range), and a token written there is
+ *   dropped (see bca_paged_status).
+ *
+ * Everything named "device" below is read by the kernels when they run, so it may be
+ * rewritten between replays of a captured graph.  Such values are never trusted for
+ * addressing: offsets are clamped to the given row count, key ranges to the table's width,
+ * page numbers are checked.  All calls are asynchronous on `stream`, allocate nothing and
+ * must be made with the cache's device current (BCA_ERR_INVALID_ARGUMENT otherwise). */
+#define BCA_PAGE_TOKENS 128
+#define BCA_PAGED_FP16 0x80u /* bca_paged_desc.flags: q, k, v, o and v_pages are fp16 */
+
+typedef struct {
+    int32_t num_q_heads;  /* Hq */
+    int32_t num_kv_heads; /* Hkv; Hq % Hkv == 0 */
+    int32_t head_dim;     /* D in {24, 32, 48} */
+    int32_t num_layers;   /* pools back to back (only bca_paged_copy looks at it) */
+    int64_t num_pages;    /* pages of one pool */
+    float rope_base[3];   /* RoPE base per axis (t, h, w) */
+    float norm_eps;       /* QK-Norm epsilon */
+    uint32_t flags;       /* BCA_PAGED_FP16 | BCA_O_FP32 | BCA_PLAN_HOST_ONLY | BCA_TEST_FORCE_TIMEOUT */
+} bca_paged_desc;
+
+typedef struct bca_paged_s *bca_paged_t;
+
+int bca_paged_create(const bca_paged_desc *desc, bca_paged_t *out);
+void bca_paged_destroy(bca_paged_t cache);
+
+/* Bytes of one layer's K pool, which are also those of its V pool. */
+size_t bca_paged_pool_bytes(bca_paged_t cache);
+
+/* Write new tokens into their pages.  Rows off[b] .. off[b+1]-1 of k and v belong to table
+ * row b and become its tokens start[b], start[b] + 1, ...  (appending, or overwriting the
+ * tokens of a window that is denoised again).
+ *   k, v   : io type [n][Hkv][D]
+ *   pos    : device int32 [n][3], RoPE position (t, h, w) of each row, or NULL: k is given
+ *            post-prologue and only converted to fp16 (k_gain must then be NULL)
+ *   k_gain : device fp32 [D] QK-Norm gain, or NULL (= ones)
+ *   table  : device int32 [seqs][width];  off: device int32 [seqs + 1], non-decreasing;
+ *   start  : device int32 [seqs]
+ * Rows outside every sequence are not read.  Two rows for the same slot of the same page
+ * leave either of them there.  A row whose token lies outside the table or in an absent
+ * page is dropped and recorded for bca_paged_status (BCA_ERR_BAD_PAGE). */
+int bca_paged_write(bca_paged_t cache, const void *k, const void *v, int64_t n, const int32_t *pos,
+                    const float *k_gain, const int32_t *table, int32_t seqs, int32_t width,
+                    const int32_t *off, const int32_t *start, void *k_pages, void *v_pages, void *stream);
+
+/* Copy whole pages in every layer: for each pair, page pairs[2i + 1] becomes a copy of page
+ * pairs[2i] (a forked sequence's own copy of a shared page; a page moved when a pool is
+ * compacted).  pairs: HOST int32 [n][2], read before the call returns.  k_pages, v_pages:
+ * the first layer's pools.  Every page number must lie in the pool, no page may be written
+ * twice, and no page that is written may be read by another pair (the copies run at the
+ * same time): BCA_ERR_BAD_PAGE otherwise, and nothing is copied. */
+int bca_paged_copy(bca_paged_t cache, const int32_t *pairs, int64_t n, void *k_pages, void *v_pages, void *stream);
+
+/* Attention of new tokens over the pages.  Query rows off[i] .. off[i+1]-1 are slice i: they
+ * see keys k_begin[i] .. k_end[i]-1 of table row seq[i], fully, or with causal != 0 up to
+ * their own place when the slice's last row sees the last key (BCA_SLICE_CAUSAL's rule):
+ * row r sees keys j with j <= k_end[i] - (off[i+1] - r).  Block-causal attention of a window
+ * of chunks is one slice per chunk, a KV range is the slice's k_begin, one new token of each
+ * of B videos is B slices of one row.  The new tokens' own keys have been written before.
+ *   q      : io type [nq][Hq][D];  o: the same, or fp32 with BCA_O_FP32
+ *   pos    : device int32 [nq][3] or NULL: q is given post-prologue (q_gain NULL then)
+ *   off    : device int32 [slices + 1], non-decreasing;  seq: device int32 [slices], a value
+ *            outside [0, seqs) is a slice that sees no key, or NULL: slice i reads row i;
+ *   k_begin, k_end: device int32 [slices]
+ *   lse    : fp32 [Hq][nq] natural log, or NULL (not wanted)
+ * Rows that see no key get O = 0 and LSE = -inf; rows of q outside every slice are neither
+ * read nor written.  What pages hold outside a row's own keys never reaches the row, NaN and
+ * infinities included.  workspace: bca_paged_workspace_bytes bytes, 16-byte aligned; calls
+ * that may overlap on the GPU need one each.  Results do not depend on timing: the same call
+ * gives the same bits. */
+size_t bca_paged_workspace_bytes(bca_paged_t cache, int64_t nq, int32_t slices);
+int bca_paged_attend(bca_paged_t cache, const void *q, int64_t nq, const int32_t *pos, const float *q_gain,
+                     const void *k_pages, const void *v_pages, const int32_t *table, int32_t seqs,
+                     int32_t width, const int32_t *off, const int32_t *seq, const int32_t *k_begin,
+                     const int32_t *k_end, int32_t slices, int causal, void *o, float *lse, void *workspace,
+                     void *stream);
+
+/* Device status word of the cache, as bca_status: a wait that ran out
+ * (BCA_ERR_DEVICE_TIMEOUT) or written tokens without a page (BCA_ERR_BAD_PAGE). */
+int bca_paged_status(bca_paged_t cache, void *stream);
 
 const char *bca_error_string(int code);
 
