@@ -12,8 +12,8 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbca.so")
 SOURCES = ["api.cpp", "plan.cpp", "fwd.cu", "fwd_static.cu", "bwd.cu", "cp_passes.cu", "paged_api.cpp", "paged.cu",
-           "paged_rows.cu"]
-HEADERS = ["plan.hpp", "kernels.hpp", "sm100.cuh", "prologue.cuh", "paged.hpp", "paged_device.cuh"]
+           "paged_rows.cu", "paged_tiles.cu"]
+HEADERS = ["plan.hpp", "kernels.hpp", "sm100.cuh", "prologue.cuh", "paged.hpp", "paged_device.cuh", "paged_mma.cuh"]
 ARCH = ["-gencode", "arch=compute_100a,code=sm_100a"]
 NVCC_FLAGS = ARCH + ["-O3", "-lineinfo", "-std=c++17", "--expt-relaxed-constexpr",
                      "-Xcompiler", "-fPIC,-O2,-Wall", "-I", os.path.join(ROOT, "include")]

@@ -235,7 +235,6 @@ int launch_copy(const CopyArgs &a, const PagedCache &c, const int32_t *pairs, in
 // row at a time.
 
 constexpr int kJoinThreads = 512;
-constexpr int kJoinRows = 16;
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a) {
@@ -249,8 +248,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     if (!found || cur.start == hi || cur.start < lo) return;
     const uint64_t end = cur.end();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / 8, e = lane % 8;
-    for (int row = blockIdx.y * kJoinRows + warp; row < min((int)(blockIdx.y + 1) * kJoinRows, a.rows);
-         row += kJoinThreads / 32) {
+    const int rows = a.rows / gridDim.y;
+    for (int row = blockIdx.y * rows + warp; row < (int)(blockIdx.y + 1) * rows; row += kJoinThreads / 32) {
         const int64_t packed = cur.t * a.rows + row;
         if (packed / a.group >= cur.s.n) continue;
         float ref = -INFINITY, sum = 0.f, o[D / 8] = {};
@@ -306,7 +305,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 template <int D, typename T>
 int launch_join(const PagedArgs &a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.shares, (unsigned)((a.rows + kJoinRows - 1) / kJoinRows));
+    cfg.gridDim = dim3((unsigned)a.shares, (unsigned)(a.rows <= 64 ? a.rows / 16 : 6));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};
@@ -336,7 +335,7 @@ PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices) {
     PagedShape s;
     // packed rows of an average slice
     const int64_t rows = nq * (c.hq / c.hkv) / std::max(slices, 1);
-    s.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : 64;
+    s.rows = rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : kPagedTileRows;
     s.shares = kSMs;
     return s;
 }
@@ -346,7 +345,10 @@ size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices) {
     return (size_t)s.shares * 2 * s.rows * (c.d + 2) * sizeof(float);
 }
 
-int prepare_paged(const PagedCache &c) { return prepare_paged_rows(c); }
+int prepare_paged(const PagedCache &c) {
+    const int rc = prepare_paged_rows(c);
+    return rc == BCA_OK ? prepare_paged_tiles(c) : rc;
+}
 
 int launch_paged_write(const PagedCache &c, const PagedWriteIO &io, cudaStream_t stream) {
     WriteArgs a;
@@ -433,7 +435,7 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
     // the row of items must stay below 2^62 long (rows of q and tables this large do not fit a GPU)
     const double tiles = (double)io.nq * a.group / a.rows + io.slices;
     if (tiles * c.hkv * ((double)io.width * kPage + (double)io.nq + kItemWeight) > 4e18) return BCA_ERR_TOO_LARGE;
-    const int rc = launch_paged_rows(c, a, stream);
+    const int rc = a.rows == kPagedTileRows ? launch_paged_tiles(c, a, stream) : launch_paged_rows(c, a, stream);
     if (rc != BCA_OK) return rc;
     return by_type(c, [&](auto d, auto t) { return launch_join<decltype(d)::value, decltype(t)>(a, stream); });
 }

@@ -12,6 +12,7 @@ namespace bca {
 
 constexpr int kPage = BCA_PAGE_TOKENS;
 constexpr int kSMs = 148;
+constexpr int kPagedTileRows = 384;  // packed rows of a work item of paged_tiles.cu
 
 // status-word bits written by the paged kernels
 constexpr int kPagedTimeout = 0x1;
@@ -75,6 +76,8 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
 struct PagedArgs;
 int prepare_paged_rows(const PagedCache &c);
 int launch_paged_rows(const PagedCache &c, const PagedArgs &a, cudaStream_t stream);
+int prepare_paged_tiles(const PagedCache &c);
+int launch_paged_tiles(const PagedCache &c, const PagedArgs &a, cudaStream_t stream);
 
 }  // namespace bca
 

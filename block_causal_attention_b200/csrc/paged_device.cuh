@@ -238,6 +238,44 @@ __device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, bool at_
     return true;
 }
 
+// What the warps of a block need to know of the item they are at: written by the warp that
+// walks the row of items (and loads their pages), a few items ahead, so that the others
+// neither hold a cursor in registers nor wait for the loads of the next slice.
+constexpr int kItemRing = 4;
+
+struct PagedItem {
+    int32_t p0, p1;       // pages, p0 < 0: there are no more items
+    int32_t row;          // of q, the slice's first
+    int32_t token, head;  // the tile's first packed row: token of the slice, head of the group
+    int32_t left;         // packed rows from there to the slice's end (at most `rows`)
+    int32_t g;            // KV head
+    int32_t kb, ke, back; // keys [kb, ke); the causal rule: row `token` sees j < token + back too
+    int32_t whole, part;  // all of its pages are here; else the slot for this piece
+
+    // First key that a packed row of the tile does not see.
+    __device__ __forceinline__ int32_t limit(int r, int group) const {
+        // unsigned: rows behind the last wrap around
+        return min(ke, (int32_t)((uint32_t)token + (uint32_t)(head + r) / (uint32_t)group + (uint32_t)back));
+    }
+};
+
+__device__ __forceinline__ void paged_item(const PagedArgs &a, const PagedCursor &cur, int c, uint64_t lo,
+                                           uint64_t hi, PagedItem &x) {
+    cur.pages(a, lo, hi, x.p0, x.p1);
+    const int64_t first = cur.t * a.rows;
+    x.row = cur.s.r0;
+    x.token = (int32_t)(first / a.group);
+    x.head = (int32_t)(first % a.group);
+    x.left = (int32_t)min((int64_t)cur.s.n * a.group - first, (int64_t)a.rows);
+    x.g = cur.g;
+    x.kb = cur.s.kb;
+    x.ke = cur.s.ke;
+    // token + back <= end and >= -2^31, and without the causal rule never below ke
+    x.back = a.causal ? cur.s.end - (cur.s.n - 1) : INT32_MAX - cur.s.n;
+    x.whole = lo <= cur.start && cur.end() <= hi;
+    x.part = 2 * c + (lo <= cur.start ? 1 : 0);
+}
+
 __device__ __forceinline__ float *paged_part(const PagedArgs &a, int d, int slot) {
     return a.part + (size_t)slot * a.rows * (d + 2);
 }
@@ -343,6 +381,73 @@ __device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, const 
     atomicOr(a.status, kPagedTimeout);
     *abort_flag = 1;
     return false;
+}
+
+// The warp that walks the items: publishes each and moves its pages into the ring, a page's
+// keys and values by one bulk copy each, until the block's stretch ends; then waits for the
+// copies that are still in flight.  Barriers: full / empty of the STAGES page stages (base +
+// 8 i, base + 8 (STAGES + i)), and of the kItemRing items behind them.  here[i]: stage i holds
+// a page; an absent one holds no keys.
+template <int STAGES, int TILE, int KSTAGE, int STAGE>
+__device__ __forceinline__ void paged_fill(const PagedArgs &a, PagedCursor &cur, int c, uint64_t lo, uint64_t hi,
+                                           uint32_t ring, uint32_t bars, uint32_t item_bars, PagedItem *items,
+                                           volatile int *here, volatile int *abort_flag) {
+    const int lane = threadIdx.x & 31;
+    auto full = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)i; };
+    auto empty = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)(STAGES + i); };
+    int it = 0;
+    bool ok = true, more = true;
+    for (int n = 0; ok; ++n) {
+        const int slot = n % kItemRing;
+        if (n >= kItemRing)
+            ok = __all_sync(0xffffffffu, paged_wait(item_bars + 8u * (uint32_t)(kItemRing + slot),
+                                                    (n / kItemRing - 1) & 1, a, abort_flag));
+        if (!ok) break;
+        PagedItem x;
+        if (more) paged_item(a, cur, c, lo, hi, x);
+        else x.p0 = -1;
+        if (lane == 0) {
+            items[slot] = x;
+            sm100::mbar_arrive(item_bars + 8u * (uint32_t)slot);
+        }
+        if (!more) break;
+        const int32_t *row = a.table + (int64_t)cur.s.b * a.width;
+        for (int32_t base = x.p0; base < x.p1 && ok && !a.skip_loads; base += 32) {
+            const int32_t mine = base + lane < x.p1 ? __ldg(row + base + lane) : -1;
+            const int count = min(32, x.p1 - base);
+            for (int j = 0; j < count; ++j) {
+                const int32_t page = __shfl_sync(0xffffffffu, mine, j);
+                if (lane == 0 && ok) {
+                    const int st = it % STAGES;
+                    if (it >= STAGES) ok = paged_wait(empty(st), (it / STAGES - 1) & 1, a, abort_flag);
+                    if (ok) {
+                        const bool on = page >= 0 && page < a.pages;
+                        here[st] = on;
+                        if (on) {
+                            const int64_t at = ((int64_t)page * a.hkv + x.g) * TILE;
+                            const uint32_t dst = ring + st * STAGE;
+                            sm100::mbar_arrive_expect_tx(full(st), 2 * TILE);
+                            sm100::bulk_g2s(dst, static_cast<const uint8_t *>(a.k_pages) + at, TILE, full(st));
+                            sm100::bulk_g2s(dst + KSTAGE, static_cast<const uint8_t *>(a.v_pages) + at, TILE, full(st));
+                        } else {
+                            sm100::mbar_arrive(full(st));
+                        }
+                        ++it;
+                    }
+                }
+            }
+            ok = __shfl_sync(0xffffffffu, ok, 0);
+        }
+        more = cur.end() < hi && cur.next(a);
+    }
+    // every copy must have landed before the block may end
+    if (lane == 0)
+        for (int j = it > STAGES ? it - STAGES : 0; j < it; ++j)
+            if (!sm100::mbar_wait(full(j % STAGES), (j / STAGES) & 1, a.timeout_ns)) {
+                atomicOr(a.status, kPagedTimeout);
+                *abort_flag = 1;
+            }
+    __syncwarp();
 }
 
 }  // namespace bca

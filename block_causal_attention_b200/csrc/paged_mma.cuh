@@ -1,0 +1,112 @@
+// The warps' own matrix instructions over page tiles, and what a page's slots that a row does
+// not see need: shared by the kernels of paged attention.
+#pragma once
+
+#include "paged_device.cuh"
+
+namespace bca {
+
+__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void ldsm2(uint32_t addr, uint32_t &r0, uint32_t &r1) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr) : "memory");
+}
+
+// V of 16 tokens: vf[n] is the B operand of channels 8 n .. 8 n + 7 (lane (g, t): channel g,
+// tokens 2 t, 2 t + 1 and 8 more).  addr: the lane's row, token group (lane / 8) % 2, channel
+// group lane / 16.
+template <int NV>
+__device__ __forceinline__ void ldsm_v(uint32_t addr, uint32_t (&vf)[NV][2]) {
+#pragma unroll
+    for (int n = 0; n + 1 < NV; n += 2) {
+        uint32_t r[4];
+        ldsm4(addr + n * 128, r);
+        vf[n][0] = r[0];
+        vf[n][1] = r[1];
+        vf[n + 1][0] = r[2];
+        vf[n + 1][1] = r[3];
+    }
+    if constexpr (NV % 2 == 1) ldsm2(addr + (NV - 1) * 128, vf[NV - 1][0], vf[NV - 1][1]);
+}
+
+// c += a b, 16 x 8 x 16, fp32 sums
+template <bool F16>
+__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    if constexpr (F16)
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    else
+        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void mma8_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
+    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(b0));
+}
+
+// A weight of 0 does not silence a NaN or an infinity.  So, where some row does not see all of
+// the 16 tokens whose V is in vf: tokens that no row sees (outside [kb, end)) are cleared, and
+// so is every value that is not finite; true (for the whole warp) if there was one, and then
+// add_left_out gives it to the rows that do see it.  key: that of the lane's first token.
+template <typename T, int NV>
+__device__ __forceinline__ bool clear_unseen(uint32_t (&vf)[NV][2], int32_t key, int32_t kb, int32_t end) {
+    bool odd = false;
+#pragma unroll
+    for (int b = 0; b < 2; ++b) {
+        const int32_t k = key + 8 * b;
+        const uint32_t keep = (k >= kb && k < end ? 0xffffu : 0u) | (k + 1 >= kb && k + 1 < end ? 0xffff0000u : 0u);
+#pragma unroll
+        for (int n = 0; n < NV; ++n) {
+            uint32_t v = vf[n][b] & keep;
+            if (Io<T>::bad(v)) {
+                odd = true;
+                v &= 0xffff0000u;
+            }
+            if (Io<T>::bad(v >> 16)) {
+                odd = true;
+                v &= 0xffffu;
+            }
+            vf[n][b] = v;
+        }
+    }
+    return __any_sync(0xffffffffu, odd);
+}
+
+// o += p v over the values that clear_unseen left out, for the rows that see their token: p0,
+// p1 the weights of tokens 0 .. 7 and 8 .. 15 in accumulator layout, v the two token groups in
+// shared memory, lim where the lane's two rows' keys end.  Rare, so written for size; inlined, since
+// arrays handed to a function that is not live in memory.
+template <int D, typename T, int NV>
+__device__ __forceinline__ void add_left_out(float (&o)[NV][4], const float (&p0)[4], const float (&p1)[4], const T *v,
+                                          int32_t key0, int32_t kb, const int32_t (&lim)[2]) {
+    const int lane = threadIdx.x & 31, t = lane & 3;
+#pragma unroll 1
+    for (int x = 0; x < 16; ++x) {
+        const int src = (lane & ~3) + (x % 8) / 2;
+        float w[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const float even = __shfl_sync(0xffffffffu, x < 8 ? p0[2 * h] : p1[2 * h], src);
+            const float odd = __shfl_sync(0xffffffffu, x < 8 ? p0[2 * h + 1] : p1[2 * h + 1], src);
+            w[h] = x % 2 ? odd : even;
+        }
+        const int32_t key = key0 + x;
+#pragma unroll
+        for (int n = 0; n < NV; ++n)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const T y = v[(x / 8 * D + 8 * n + 2 * t + (j & 1)) * 8 + x % 8];
+                if (Io<T>::bad(*reinterpret_cast<const uint16_t *>(&y)) && key >= kb && key < lim[j >> 1])
+                    o[n][j] += w[j >> 1] * (float)y;
+            }
+    }
+}
+
+}  // namespace bca

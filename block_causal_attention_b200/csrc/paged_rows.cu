@@ -19,6 +19,7 @@
 #include <type_traits>
 
 #include "paged_device.cuh"
+#include "paged_mma.cuh"
 
 namespace bca {
 
@@ -39,39 +40,25 @@ struct RowsSmem {
     static constexpr int OFF_Q = STAGES * 2 * TILE;
     static constexpr int OFF_MERGE = OFF_Q + 64 * QSTRIDE * 2;
     static constexpr int OFF_BAR = OFF_MERGE + kWarps * 16 * (D + 2) * 4;
-    static constexpr int OFF_HERE = OFF_BAR + 2 * STAGES * 8;
-    static constexpr int OFF_ABORT = OFF_HERE + STAGES * 4;
+    static constexpr int OFF_HERE = OFF_BAR + 2 * (STAGES + kItemRing) * 8;
+    static constexpr int OFF_ITEMS = OFF_HERE + STAGES * 4;
+    static constexpr int OFF_ABORT = OFF_ITEMS + kItemRing * (int)sizeof(PagedItem);
     static constexpr int BYTES = OFF_ABORT + 4;
 };
 
 __device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
-
-__device__ __forceinline__ void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
-                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
-}
-__device__ __forceinline__ void ldsm2(uint32_t addr, uint32_t &r0, uint32_t &r1) {
-    asm volatile("ldmatrix.sync.aligned.m8n8.x2.shared.b16 {%0,%1}, [%2];" : "=r"(r0), "=r"(r1) : "r"(addr) : "memory");
-}
-
-// c += a b, 16 x 8 x 16, fp32 sums
-template <bool F16>
-__device__ __forceinline__ void mma16(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    if constexpr (F16)
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    else
-        asm("mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
-            : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
-__device__ __forceinline__ void mma8_f16(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t b0) {
-    asm("mma.sync.aligned.m16n8k8.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5}, {%6}, {%0,%1,%2,%3};"
-        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-        : "r"(a0), "r"(a1), "r"(b0));
+// The same, and whether all of them said yes.
+__device__ __forceinline__ bool consumers_all(bool yes) {
+    uint32_t all;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t"
+        "setp.ne.b32 p, %1, 0;\n\t"
+        "bar.red.and.pred q, 1, 256, p;\n\t"
+        "selp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(all)
+        : "r"((uint32_t)yes)
+        : "memory");
+    return all != 0;
 }
 
 // MT: 16-row matrix tiles a work tile has (rows = 16 MT).
@@ -91,6 +78,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
     volatile int *here = reinterpret_cast<volatile int *>(smem + L::OFF_HERE);
     auto full = [&](int i) -> uint32_t { return sbase + L::OFF_BAR + 8u * (uint32_t)i; };
+    const uint32_t item_bars = sbase + L::OFF_BAR + 8u * (2 * S);
+    PagedItem *items = reinterpret_cast<PagedItem *>(smem + L::OFF_ITEMS);
     auto empty = [&](int i) -> uint32_t { return sbase + L::OFF_BAR + 8u * (uint32_t)(S + i); };
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
@@ -102,6 +91,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
             mbar_init(full(i), 1);
             mbar_init(empty(i), kWarps);
         }
+        for (int i = 0; i < kItemRing; ++i) {
+            mbar_init(item_bars + 8u * i, 1);
+            mbar_init(item_bars + 8u * (kItemRing + i), kWarps);
+        }
         mbar_fence_init();
     }
     PagedCursor cur;
@@ -111,48 +104,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     __syncthreads();
 
     if (warp == kWarps) {
-        // ------------------------------------------------ fills the ring
-        int it = 0;
-        bool ok = !a.skip_loads;
-        do {
-            int32_t p0, p1;
-            cur.pages(a, lo, hi, p0, p1);
-            const int32_t *row = a.table + (int64_t)cur.s.b * a.width;
-            for (int32_t base = p0; base < p1 && ok; base += 32) {
-                const int32_t mine = base + lane < p1 ? __ldg(row + base + lane) : -1;
-                const int count = min(32, p1 - base);
-                for (int j = 0; j < count; ++j) {
-                    const int32_t page = __shfl_sync(0xffffffffu, mine, j);
-                    if (lane == 0 && ok) {
-                        const int st = it % S;
-                        if (it >= S) ok = paged_wait(empty(st), (it / S - 1) & 1, a, abort_flag);
-                        if (ok) {
-                            const bool on = page >= 0 && page < a.pages;
-                            here[st] = on;
-                            if (on) {
-                                const int64_t at = ((int64_t)page * a.hkv + cur.g) * L::TILE;
-                                const uint32_t dst = sbase + L::OFF_RING + st * 2 * L::TILE;
-                                mbar_arrive_expect_tx(full(st), 2 * L::TILE);
-                                bulk_g2s(dst, static_cast<const uint8_t *>(a.k_pages) + at, L::TILE, full(st));
-                                bulk_g2s(dst + L::TILE, static_cast<const uint8_t *>(a.v_pages) + at, L::TILE,
-                                         full(st));
-                            } else {
-                                mbar_arrive(full(st));
-                            }
-                            ++it;
-                        }
-                    }
-                }
-                ok = __shfl_sync(0xffffffffu, ok, 0);
-            }
-        } while (ok && cur.end() < hi && cur.next(a));
-        // every copy must have landed before the block may end
-        if (lane == 0)
-            for (int j = it > S ? it - S : 0; j < it; ++j)
-                if (!mbar_wait(full(j % S), (j / S) & 1, a.timeout_ns)) {
-                    atomicOr(a.status, kPagedTimeout);
-                    *abort_flag = 1;
-                }
+        paged_fill<S, L::TILE, L::TILE, 2 * L::TILE>(a, cur, c, lo, hi, sbase + L::OFF_RING, full(0), item_bars, items,
+                                                     here, abort_flag);
         return;
     }
 
@@ -166,28 +119,31 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     const uint32_t vaddr = ((2 * warp + (lane >> 3 & 1)) * D + 8 * (lane >> 4) + (lane & 7)) * 16;
     bool ok = true;
     int it = 0;
-    do {
-        int32_t p0, p1;
-        cur.pages(a, lo, hi, p0, p1);
-        const bool whole = lo <= cur.start && cur.end() <= hi;
+    for (int n_item = 0;; ++n_item) {
+        // A wait that ran out ends the block here, for all warps alike: they meet in barriers below.
+        const int slot = n_item % kItemRing;
+        if (ok) ok = paged_wait(item_bars + 8u * slot, (n_item / kItemRing) & 1, a, abort_flag);
+        if (!consumers_all(ok)) break;
+        const PagedItem &x = items[slot];
+        const int32_t p0 = x.p0, p1 = x.p1, kb = x.kb;
+        if (p0 < 0) break;
 
         // queries: QK-Norm and RoPE, fp16 (|q_hat| <= sqrt(D) max|gain|; 11 bits of significand
         // against bf16's 8).  The softmax scale is applied to the scores in fp32 instead, so that
         // bf16 queries given post-prologue stay exact.
         for (int r = threadIdx.x >> 3; r < R; r += kWarps * 4) {
-            const int64_t packed = cur.t * R + r;
-            const int64_t token = packed / a.group;
             const int e = lane & 7;
-            Row8<D> x;
-            const bool live = token < cur.s.n;  // the same for the eight lanes of a row
-            const int64_t row = cur.s.r0 + (live ? token : 0);
-            x.load(static_cast<const T *>(a.q) + (row * a.hq + cur.g * a.group + packed % a.group) * D, e);
-            if (a.pos) x.prologue(a.pos + row * 3, a.q_gain, a.turns, a.eps, e);
+            const bool live = r < x.left;  // the same for the eight lanes of a row
+            const uint32_t packed = x.head + (live ? r : 0);
+            const int64_t row = x.row + x.token + (int32_t)(packed / a.group);
+            Row8<D> q;
+            q.load(static_cast<const T *>(a.q) + (row * a.hq + x.g * a.group + packed % a.group) * D, e);
+            if (a.pos) q.prologue(a.pos + row * 3, a.q_gain, a.turns, a.eps, e);
 #pragma unroll
             for (int i = 0; i < Row8<D>::N; ++i)
                 if (e + 8 * i < D / 2)
                     *reinterpret_cast<uint32_t *>(qs + r * L::QSTRIDE + 2 * (e + 8 * i)) =
-                        live ? pack_f16x2(x.x[i].x, x.x[i].y) : 0u;
+                        live ? pack_f16x2(q.x[i].x, q.x[i].y) : 0u;
         }
         consumers_sync();
         uint32_t qa[MT][KS][4], qt[MT][2];
@@ -205,15 +161,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
             qt[m][0] = TAIL ? *reinterpret_cast<const uint32_t *>(q0 + 16 * KS) : 0u;
             qt[m][1] = TAIL ? *reinterpret_cast<const uint32_t *>(q1 + 16 * KS) : 0u;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const int64_t token = (cur.t * R + 16 * m + g + 8 * h) / a.group;
-                lim[m][h] = token < cur.s.n ? paged_limit(a, cur.s, (int32_t)token) : 0;
-            }
+            for (int h = 0; h < 2; ++h) lim[m][h] = x.limit(16 * m + g + 8 * h, a.group);
         }
         // keys that every row of the tile sees end here, and those that any row sees there
-        const int32_t lim_all = paged_limit(a, cur.s, (int32_t)(cur.t * R / a.group));
-        const int32_t lim_any = paged_limit(
-            a, cur.s, (int32_t)min(((cur.t + 1) * R - 1) / a.group, (int64_t)cur.s.n - 1));
+        const int32_t lim_all = x.limit(0, a.group), lim_any = x.limit(x.left - 1, a.group);
 
         float o[MT][NV][4], ref[MT][2], sum[MT][2];
 #pragma unroll
@@ -231,49 +182,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
             if (ok) ok = __all_sync(0xffffffffu, paged_wait(full(st), (it / S) & 1, a, abort_flag));
             if (!ok) break;
             const int32_t key0 = p * kPage + warp * kWarpTokens;
-            if (here[st] && key0 + kWarpTokens > cur.s.kb && key0 < lim_any) {
+            if (here[st] && key0 + kWarpTokens > kb && key0 < lim_any) {
                 const uint32_t ks = sbase + L::OFF_RING + st * 2 * L::TILE, vs = ks + L::TILE;
                 uint32_t kf[KS][4], kt[2] = {0, 0}, vf[NV][2];
 #pragma unroll
                 for (int k = 0; k < KS; ++k) ldsm4(ks + kaddr + k * (2 * kPage * 16), kf[k]);
                 if constexpr (TAIL)
                     ldsm2(ks + KS * (2 * kPage * 16) + (2 * warp + (lane >> 3 & 1)) * 128 + (lane & 7) * 16, kt[0], kt[1]);
-#pragma unroll
-                for (int n = 0; n + 1 < NV; n += 2) {
-                    uint32_t r[4];
-                    ldsm4(vs + vaddr + n * 128, r);
-                    vf[n][0] = r[0];
-                    vf[n][1] = r[1];
-                    vf[n + 1][0] = r[2];
-                    vf[n + 1][1] = r[3];
-                }
-                if constexpr (NV % 2 == 1) ldsm2(vs + vaddr + (NV - 1) * 128, vf[NV - 1][0], vf[NV - 1][1]);
+ldsm_v<NV>(vs + vaddr, vf);
 
-                const bool inside = key0 >= cur.s.kb && key0 + kWarpTokens <= lim_all;
+                const bool inside = key0 >= kb && key0 + kWarpTokens <= lim_all;
                 bool odd = false;  // values that are not finite, at keys that some rows do not see
-                if (!inside) {
-                    // a weight of 0 does not silence a NaN or an infinity: what no row sees is cleared
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const int32_t key = key0 + 8 * b + 2 * t;
-                        const uint32_t keep = (key >= cur.s.kb && key < lim_any ? 0xffffu : 0u) |
-                                              (key + 1 >= cur.s.kb && key + 1 < lim_any ? 0xffff0000u : 0u);
-#pragma unroll
-                        for (int n = 0; n < NV; ++n) {
-                            uint32_t v = vf[n][b] & keep;
-                            if (Io<T>::bad(v)) {
-                                odd = true;
-                                v &= 0xffff0000u;
-                            }
-                            if (Io<T>::bad(v >> 16)) {
-                                odd = true;
-                                v &= 0xffffu;
-                            }
-                            vf[n][b] = v;
-                        }
-                    }
-                    odd = __any_sync(0xffffffffu, odd);
-                }
+                if (!inside) odd = clear_unseen<T, NV>(vf, key0 + 2 * t, kb, lim_any);
 #pragma unroll
                 for (int m = 0; m < MT; ++m) {
                     float s[2][4] = {};
@@ -292,7 +212,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const int32_t key = key0 + 8 * n + 2 * t + (j & 1);
-                                if (key < cur.s.kb || key >= lim[m][j >> 1]) s[n][j] = -INFINITY;
+                                if (key < kb || key >= lim[m][j >> 1]) s[n][j] = -INFINITY;
                             }
                     }
                     float mx[2];
@@ -332,31 +252,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
                                             Io<T>::pack(s[1][0], s[1][1]), Io<T>::pack(s[1][2], s[1][3])};
 #pragma unroll
                     for (int n = 0; n < NV; ++n) mma16<Io<T>::kF16>(o[m][n], pa, vf[n][0], vf[n][1]);
-                    if (odd) {
-                        // the values left out above, for the rows that do see their key
-                        const T *v = reinterpret_cast<const T *>(smem + L::OFF_RING + st * 2 * L::TILE + L::TILE);
-#pragma unroll 1
-                        for (int x = 0; x < kWarpTokens; ++x) {
-                            const int src = (lane & ~3) + (x % 8) / 2;
-                            float w[2];
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                const float even = __shfl_sync(0xffffffffu, x < 8 ? s[0][2 * h] : s[1][2 * h], src);
-                                const float odd_ = __shfl_sync(0xffffffffu, x < 8 ? s[0][2 * h + 1] : s[1][2 * h + 1], src);
-                                w[h] = x % 2 ? odd_ : even;
-                            }
-                            const int32_t key = key0 + x;
-#pragma unroll
-                            for (int n = 0; n < NV; ++n)
-#pragma unroll
-                                for (int j = 0; j < 4; ++j) {
-                                    const T y = v[((2 * warp + x / 8) * D + 8 * n + 2 * t + (j & 1)) * 8 + x % 8];
-                                    if (Io<T>::bad(*reinterpret_cast<const uint16_t *>(&y)) && key >= cur.s.kb &&
-                                        key < lim[m][j >> 1])
-                                        o[m][n][j] += w[j >> 1] * (float)y;
-                                }
-                        }
-                    }
+                    if (odd)
+                        add_left_out<D, T, NV>(o[m], s[0], s[1],
+                                               reinterpret_cast<const T *>(smem + (vs - sbase)) + 2 * warp * D * 8, key0,
+                                               kb, lim[m]);
                 }
             }
             __syncwarp();
@@ -390,21 +289,21 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
             float l = 0.f, y[(D + 15) / 16] = {};
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float *x = row + w * 16 * (D + 2);
-                const float mul = top == -INFINITY ? 0.f : ex2(x[D] - top);
-                l = fmaf(x[D + 1], mul, l);
+                const float *in = row + w * 16 * (D + 2);
+                const float mul = top == -INFINITY ? 0.f : ex2(in[D] - top);
+                l = fmaf(in[D + 1], mul, l);
 #pragma unroll
                 for (int i = 0; i < (D + 15) / 16; ++i)
-                    if (e + 16 * i < D) y[i] = fmaf(x[e + 16 * i], mul, y[i]);
+                    if (e + 16 * i < D) y[i] = fmaf(in[e + 16 * i], mul, y[i]);
             }
-            const int64_t packed = cur.t * R + 16 * m + r;
-            const int64_t token = packed / a.group;
-            if (token < cur.s.n) {
-                if (whole) {
+            if (16 * m + r < x.left) {
+                if (x.whole) {
                     const bool none = top == -INFINITY;
                     const float inv = none ? 0.f : 1.f / l;
-                    const int head = cur.g * a.group + (int)(packed % a.group);
-                    const int64_t at = ((cur.s.r0 + token) * a.hq + head) * D;
+                    const uint32_t packed = x.head + 16 * m + r;
+                    const int64_t token = x.row + x.token + (int32_t)(packed / a.group);
+                    const int head = x.g * a.group + (int)(packed % a.group);
+                    const int64_t at = (token * a.hq + head) * D;
 #pragma unroll
                     for (int i = 0; i < (D + 15) / 16; ++i) {
                         if (e + 16 * i >= D) continue;
@@ -413,10 +312,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
                         else static_cast<T *>(a.o)[at + e + 16 * i] = T(z);
                     }
                     if (a.lse && e == 0)
-                        a.lse[head * a.nq + cur.s.r0 + token] =
+                        a.lse[head * a.nq + token] =
                             none ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
                 } else if (p0 < p1) {
-                    float *part = paged_part(a, D, 2 * c + (lo <= cur.start ? 1 : 0));
+                    float *part = paged_part(a, D, x.part);
 #pragma unroll
                     for (int i = 0; i < (D + 15) / 16; ++i)
                         if (e + 16 * i < D) part[(16 * m + r) * D + e + 16 * i] = y[i];
@@ -428,7 +327,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
             }
             consumers_sync();
         }
-    } while (cur.end() < hi && cur.next(a));
+        if (lane == 0) mbar_arrive(item_bars + 8u * (kItemRing + slot));
+    }
 }
 
 template <int D, typename T>

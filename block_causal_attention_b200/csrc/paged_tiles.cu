@@ -1,0 +1,474 @@
+// Attention of many packed rows (chunks of new tokens) over the pages of a KV cache.
+//
+// The mathematics of paged_rows.cu.  Bound by the special-function units: one exponential a
+// score, 16 a clock and multiprocessor, against 4 D operations on tensor cores that would do
+// twice that many scores.  So the exponentials must never wait:
+//   - S = Q K^T by tcgen05.mma (128 x 128 tiles, fp32 in tensor memory), issued by one thread
+//     that runs ahead: three tiles of 128 rows share each page, every tile has its own S;
+//   - S comes back to the registers in the fragment layout of the warps' matrix instruction
+//     (tcgen05.ld.16x256b), so that P needs no way through shared or tensor memory: O += P V
+//     is a warp's own mma.sync with O in registers.  A PV product by tcgen05 has N = D <= 48
+//     and takes the tensor pipe as long as N = 128 would; worse, its completion stands between
+//     two softmax steps.  Here a softmax warp waits for one thing a page, its next S, which has
+//     been ready for long;
+//   - 12 softmax warps, three a scheduler: one's maxima and products run under another's
+//     exponentials.
+#include <cuda_runtime.h>
+
+#include <type_traits>
+
+#include "paged_device.cuh"
+#include "paged_mma.cuh"
+
+namespace bca {
+
+using namespace sm100;
+
+namespace {
+
+constexpr int kSlots = 3;                  // 128-row tiles that share a page
+constexpr int kRows = kPagedTileRows;
+constexpr int kThreads = 128 + 128 * kSlots;
+static_assert(kRows == 128 * kSlots, "rows of a work item");
+
+template <int D>
+struct TilesSmem {
+    static constexpr int DPAD = Geo<D>::DPAD;
+    static constexpr int TILE = D * kPage * 2;       // bytes of a page's K or V of one head
+    static constexpr int KSTAGE = DPAD * kPage * 2;  // K is padded to whole 16-channel steps
+    static constexpr int STAGE = KSTAGE + TILE;
+    static constexpr int STAGES = D == 48 ? 6 : 8;
+    static constexpr int Q_BYTES = 128 * DPAD * 2;
+    static constexpr int OFF_Q = 0;
+    static constexpr int OFF_RING = kSlots * Q_BYTES;
+    static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE;
+    static constexpr int B_FULL = 0;
+    static constexpr int B_EMPTY = STAGES;
+    static constexpr int B_ITEM = 2 * STAGES;
+    static constexpr int B_S_FULL = B_ITEM + 2 * kItemRing;
+    static constexpr int B_S_FREE = B_S_FULL + kSlots;
+    static constexpr int B_Q = B_S_FREE + kSlots;
+    static constexpr int B_DONE = B_Q + kSlots;
+    static constexpr int OFF_HERE = OFF_BAR + 8 * (B_DONE + 1);
+    static constexpr int OFF_TMEM = OFF_HERE + 4 * STAGES;
+    static constexpr int OFF_ITEMS = OFF_TMEM + 4;
+    static constexpr int OFF_ABORT = OFF_ITEMS + kItemRing * (int)sizeof(PagedItem);
+    static constexpr int BYTES = OFF_ABORT + 4;
+};
+
+constexpr int kChunk = 32;                 // keys a softmax step takes: 32 scores a thread
+constexpr int kTiles = kChunk / 8;
+
+// Lane (g, t) of the warp gets row g, columns 8 n + 2 t and + 1 in f[n][0], f[n][1] and row
+// g + 8 in f[n][2], f[n][3]: the accumulator layout of mma.m16n8k16.
+__device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&f)[4][4]) {
+    uint32_t r[16];
+    asm volatile(
+        "tcgen05.ld.sync.aligned.16x256b.x4.b32 "
+        "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]),
+          "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]),
+          "=r"(r[15])
+        : "r"(taddr));
+#pragma unroll
+    for (int i = 0; i < 16; ++i) f[i / 4][i % 4] = __uint_as_float(r[i]);
+}
+
+template <int D, typename T>
+__global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_constant__ PagedArgs a) {
+    using L = TilesSmem<D>;
+    constexpr int S = L::STAGES;
+    constexpr int NV = D / 8;
+    constexpr uint32_t IDESC = idesc_f32acc(128, 128, kFmtF16);
+    constexpr float kShift = Io<T>::kShift;
+
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ PagedLocate sh;
+    const uint32_t sbase = smem_u32(smem);
+    auto bar = [&](int i) -> uint32_t { return sbase + L::OFF_BAR + 8u * (uint32_t)i; };
+    volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
+    volatile int *here = reinterpret_cast<volatile int *>(smem + L::OFF_HERE);
+    PagedItem *items = reinterpret_cast<PagedItem *>(smem + L::OFF_ITEMS);
+    uint32_t *tmem_ptr = reinterpret_cast<uint32_t *>(smem + L::OFF_TMEM);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    PagedCursor cur;
+    uint64_t lo, hi, total;
+    const int c = blockIdx.x;
+    if (!paged_locate(a, c, false, sh, lo, hi, total, cur)) return;
+
+    if (threadIdx.x == 0) {
+        *abort_flag = 0;
+        for (int i = 0; i < S; ++i) {
+            mbar_init(bar(L::B_FULL + i), 1);
+            mbar_init(bar(L::B_EMPTY + i), 4 * kSlots);
+        }
+        for (int s = 0; s < kSlots; ++s) {
+            mbar_init(bar(L::B_S_FULL + s), 1);
+            mbar_init(bar(L::B_S_FREE + s), 4);
+            mbar_init(bar(L::B_Q + s), 4);
+        }
+        for (int i = 0; i < kItemRing; ++i) {
+            mbar_init(bar(L::B_ITEM + i), 1);
+            mbar_init(bar(L::B_ITEM + kItemRing + i), 1 + 4 * kSlots);
+        }
+        mbar_init(bar(L::B_DONE), 1);
+        mbar_fence_init();
+    }
+    if constexpr (L::DPAD > D) {
+        // channels that do not exist: zero in Q and, so that 0 times them is 0, in every K stage
+        constexpr int N = (L::KSTAGE - L::TILE) / 16;
+        for (int i = threadIdx.x; i < (S + kSlots) * N; i += kThreads) {
+            uint8_t *to = i / N < S ? smem + L::OFF_RING + i / N * L::STAGE + L::TILE
+                                    : smem + L::OFF_Q + (i / N - S) * L::Q_BYTES + 128 * D * 2;
+            reinterpret_cast<uint4 *>(to)[i % N] = make_uint4(0, 0, 0, 0);
+        }
+    }
+    fence_proxy_async_smem();
+    if (warp == 2) {
+        tmem_alloc(smem_u32(tmem_ptr), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tmem_ptr;
+
+    // Registers: 512 threads x 128 at launch; the softmax warps take 152 (48 sums of O and 32
+    // scores among them): 128 x 56 + 384 x 152 = 65,536.
+    if (warp < 4) regs_dec<56>();
+    if (warp == 0) {
+        paged_fill<S, L::TILE, L::KSTAGE, L::STAGE>(a, cur, c, lo, hi, sbase + L::OFF_RING, bar(L::B_FULL),
+                                                    bar(L::B_ITEM), items, here, abort_flag);
+    } else if (warp == 1) {
+        // ------------------------------------------------ S = Q K^T
+        if (lane == 0) {
+            int it = 0;
+            int queries[kSlots] = {}, count[kSlots] = {};  // of each slot: query tiles and S tiles so far
+            bool ok = true;
+            for (int n = 0; ok; ++n) {
+                ok = paged_wait(bar(L::B_ITEM + n % kItemRing), (n / kItemRing) & 1, a, abort_flag);
+                if (!ok) break;
+                const int32_t p0 = items[n % kItemRing].p0, p1 = items[n % kItemRing].p1;
+                const int32_t left = items[n % kItemRing].left;
+                if (p0 < 0) break;
+                mbar_arrive(bar(L::B_ITEM + kItemRing + n % kItemRing));
+                if (p0 == p1) continue;
+#pragma unroll
+                for (int s = 0; s < kSlots; ++s)
+                    if (s * 128 < left) ok = ok && paged_wait(bar(L::B_Q + s), queries[s]++ & 1, a, abort_flag);
+                for (int32_t p = p0; p < p1 && ok; ++p, ++it) {
+                    const int st = it % S;
+                    ok = paged_wait(bar(L::B_FULL + st), (it / S) & 1, a, abort_flag);
+#pragma unroll
+                    for (int s = 0; s < kSlots; ++s) {
+                        if (!ok || s * 128 >= left) continue;
+                        if (count[s] > 0)
+                            ok = paged_wait(bar(L::B_S_FREE + s), (count[s] - 1) & 1, a, abort_flag);
+                        if (!ok) continue;
+                        ++count[s];
+                        tc_fence_after();
+                        const uint32_t qa = sbase + L::OFF_Q + s * L::Q_BYTES;
+                        const uint32_t kb = sbase + L::OFF_RING + st * L::STAGE;
+#pragma unroll
+                        for (int k = 0; k < L::DPAD / 16; ++k)
+                            mma_f16(tbase + 128 * s, smem_desc(qa + k * 4096, 2048, 128),
+                                    smem_desc(kb + k * 4096, 2048, 128), IDESC, k > 0);
+                        mma_commit(bar(L::B_S_FULL + s));
+                    }
+                }
+            }
+        }
+        if (lane == 0) {
+            // all issued products must be complete before the tensor memory is given back
+            mma_commit(bar(L::B_DONE));
+            if (!mbar_wait(bar(L::B_DONE), 0, a.timeout_ns)) {
+                atomicOr(a.status, kPagedTimeout);
+                *abort_flag = 1;
+            }
+        }
+        __syncwarp();
+    } else if (warp >= 4) {
+        regs_inc<152>();
+        // ------------------------------------------------ softmax and O += P V
+        const int slot = (warp - 4) >> 2, quarter = warp & 3;
+        const int g = lane >> 2, t = lane & 3;
+        const uint32_t tS = tbase + ((uint32_t)(quarter * 32) << 16) + 128 * slot;
+        // rows 8 j .. of matrix j: V's token group j % 2, channel group j / 2
+        const uint32_t vaddr = ((lane >> 3 & 1) * D + 8 * (lane >> 4) + (lane & 7)) * 16;
+        int it = 0, mine = 0;
+        bool ok = true;
+        const int wr = slot * 128 + quarter * 32;  // the warp's first row of the work tile
+        for (int n_item = 0; ok; ++n_item) {
+            const uint32_t done = bar(L::B_ITEM + kItemRing + n_item % kItemRing);
+            ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_ITEM + n_item % kItemRing), (n_item / kItemRing) & 1, a,
+                                                    abort_flag));
+            if (!ok) break;
+            const PagedItem &x = items[n_item % kItemRing];
+            const int32_t p0 = x.p0, p1 = x.p1;
+            if (p0 < 0) break;
+            if (slot * 128 >= x.left) {
+                for (int32_t p = p0; p < p1 && ok; ++p, ++it) {
+                    ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_FULL + it % S), (it / S) & 1, a, abort_flag));
+                    if (ok && lane == 0) mbar_arrive(bar(L::B_EMPTY + it % S));
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(done);
+                continue;
+            }
+
+            float o[2][NV][4], ref[2][2], sum[2][2];
+#pragma unroll
+            for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                for (int n = 0; n < NV; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) o[m][n][j] = 0.f;
+                ref[m][0] = ref[m][1] = -INFINITY;
+                sum[m][0] = sum[m][1] = 0.f;
+            }
+            if (p0 < p1) {
+                // queries of this warp's 32 rows, as the A operand (K-major core matrices); the slot's
+                // last S is here, so the products that read the old ones are done
+#pragma unroll 2
+                for (int i = 0; i < 8; ++i) {
+                    const int r = quarter * 32 + i * 4 + (lane >> 3), e = lane & 7;
+                    const bool live = slot * 128 + r < x.left;
+                    const uint32_t packed = x.head + (live ? slot * 128 + r : 0);
+                    const int64_t row = x.row + x.token + (int32_t)(packed / a.group);
+                    Row8<D> q;
+                    q.load(static_cast<const T *>(a.q) + (row * a.hq + x.g * a.group + packed % a.group) * D, e);
+                    if (a.pos) q.prologue(a.pos + row * 3, a.q_gain, a.turns, a.eps, e);
+#pragma unroll
+                    for (int k = 0; k < Row8<D>::N; ++k) {
+                        const int pr = e + 8 * k;
+                        if (pr < D / 2)
+                            *reinterpret_cast<uint32_t *>(smem + L::OFF_Q + slot * L::Q_BYTES + (pr >> 2) * 2048 +
+                                                          r * 16 + (pr & 3) * 4) =
+                                live ? pack_f16x2(q.x[k].x, q.x[k].y) : 0u;
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_Q + slot));
+            }
+            // keys that all, and that some of the warp's rows see end here
+            const int32_t lim_all = x.limit(min(wr, x.left - 1), a.group);
+            const int32_t lim_any = x.limit(min(wr + 31, x.left - 1), a.group);
+            const int32_t kb = x.kb;
+            for (int32_t p = p0; p < p1; ++p, ++it, ++mine) {
+                const int st = it % S;
+                if (ok)
+                    ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_FULL + st), (it / S) & 1, a, abort_flag) &&
+                                                     paged_wait(bar(L::B_S_FULL + slot), mine & 1, a, abort_flag));
+                if (!ok) break;
+                tc_fence_after();
+                const bool on = here[st];
+                const uint32_t vs = sbase + L::OFF_RING + st * L::STAGE + L::KSTAGE;
+#pragma unroll 1
+                for (int step = 0; step < kPage / kChunk; ++step) {
+                    const int32_t key0 = p * kPage + kChunk * step;
+                    const bool work = on && key0 + kChunk > kb && key0 < lim_any;
+                    float s[2][kTiles][4];
+                    if (work) {
+                        tmem_ld_frag(tS + kChunk * step, s[0]);
+                        tmem_ld_frag(tS + (16u << 16) + kChunk * step, s[1]);
+                        tmem_wait_ld();
+#pragma unroll
+                        for (int i = 0; i < 8 * kTiles; ++i)
+                            asm volatile("" : "+f"(s[i / (4 * kTiles)][i / 4 % kTiles][i % 4]));
+                    }
+                    if (step == kPage / kChunk - 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(bar(L::B_S_FREE + slot));
+                    }
+                    if (!work) continue;
+                    const bool inside = key0 >= kb && key0 + kChunk <= lim_all;
+                    if (!inside) {
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const int32_t lim = x.limit(wr + 16 * m + 8 * h + g, a.group);
+#pragma unroll
+                                for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+                                    for (int j = 0; j < 2; ++j) {
+                                        const int32_t key = key0 + 8 * n + 2 * t + j;
+                                        if (key < kb || key >= lim) s[m][n][2 * h + j] = -INFINITY;
+                                    }
+                            }
+                    }
+                    float mx[2][2];
+                    bool grow = false;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float top = s[m][0][2 * h];
+#pragma unroll
+                            for (int n = 0; n < kTiles; ++n) {
+                                top = fmaxf(top, s[m][n][2 * h]);
+                                top = fmaxf(top, s[m][n][2 * h + 1]);
+                            }
+                            mx[m][h] = top * a.scale;
+                            grow |= mx[m][h] > ref[m][h] + (kShift + kLazy);
+                        }
+                    if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                float top = mx[m][h];
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                                if (top > ref[m][h] + (kShift + kLazy)) {
+                                    const float now = top - kShift;
+                                    const float mul = ref[m][h] == -INFINITY ? 0.f : ex2(ref[m][h] - now);
+                                    ref[m][h] = now;
+                                    sum[m][h] *= mul;
+#pragma unroll
+                                    for (int n = 0; n < NV; ++n) {
+                                        o[m][n][2 * h] *= mul;
+                                        o[m][n][2 * h + 1] *= mul;
+                                    }
+                                }
+                            }
+                    }
+                    float sub[2][2];
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) sub[m][h] = ref[m][h] == -INFINITY ? 0.f : -ref[m][h];
+#pragma unroll
+                    for (int k = 0; k < kChunk / 16; ++k) {
+                        uint32_t pa[2][4];
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int b = 0; b < 2; ++b)
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    float *y = &s[m][2 * k + b][2 * h];
+                                    y[0] = ex2(fmaf(y[0], a.scale, sub[m][h]));
+                                    y[1] = ex2(fmaf(y[1], a.scale, sub[m][h]));
+                                    sum[m][h] += y[0];
+                                    sum[m][h] += y[1];
+                                    pa[m][2 * b + h] = Io<T>::pack(y[0], y[1]);
+                                }
+                        const uint32_t va = vs + (step * kTiles + 2 * k) * (D * 16) + vaddr;
+                        uint32_t vf[NV][2];
+                        ldsm_v<NV>(va, vf);
+                        bool odd = false;
+                        const int32_t keyk = key0 + 16 * k;
+                        if (!inside) odd = clear_unseen<T, NV>(vf, keyk + 2 * t, kb, lim_any);
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int n = 0; n < NV; ++n) mma16<Io<T>::kF16>(o[m][n], pa[m], vf[n][0], vf[n][1]);
+                        if (odd) {
+                            const T *v = reinterpret_cast<const T *>(smem + (vs - sbase)) + (step * kTiles + 2 * k) * D * 8;
+#pragma unroll
+                            for (int m = 0; m < 2; ++m) {
+                                int32_t lim[2];
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) lim[h] = x.limit(wr + 16 * m + 8 * h + g, a.group);
+                                add_left_out<D, T, NV>(o[m], s[m][2 * k], s[m][2 * k + 1], v, keyk, kb, lim);
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_EMPTY + st));
+            }
+
+            // ------------------------------------------------ O / l and the LSE, or this block's piece
+            float *part = paged_part(a, D, x.part);
+#pragma unroll
+            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    float l = sum[m][h];
+                    l += __shfl_xor_sync(0xffffffffu, l, 1);
+                    l += __shfl_xor_sync(0xffffffffu, l, 2);
+                    const int r = wr + 16 * m + 8 * h + g;
+                    if (r >= x.left) continue;
+                    if (x.whole) {
+                        const bool none = ref[m][h] == -INFINITY;
+                        const float inv = none ? 0.f : 1.f / l;
+                        const uint32_t packed = x.head + r;
+                        const int64_t token = x.row + x.token + (int32_t)(packed / a.group);
+                        const int head = x.g * a.group + (int)(packed % a.group);
+                        const int64_t at = (token * a.hq + head) * D + 2 * t;
+#pragma unroll
+                        for (int n = 0; n < NV; ++n) {
+                            const float y0 = none ? 0.f : o[m][n][2 * h] * inv;
+                            const float y1 = none ? 0.f : o[m][n][2 * h + 1] * inv;
+                            if (a.o_fp32)
+                                *reinterpret_cast<float2 *>(static_cast<float *>(a.o) + at + 8 * n) = make_float2(y0, y1);
+                            else
+                                *reinterpret_cast<uint32_t *>(static_cast<T *>(a.o) + at + 8 * n) = Io<T>::pack(y0, y1);
+                        }
+                        if (a.lse && t == 0)
+                            a.lse[head * a.nq + token] = none ? -INFINITY : (ref[m][h] + log2f(l)) * 0.69314718055994531f;
+                    } else if (p0 < p1) {
+#pragma unroll
+                        for (int n = 0; n < NV; ++n)
+                            *reinterpret_cast<float2 *>(part + (size_t)r * D + 8 * n + 2 * t) =
+                                make_float2(o[m][n][2 * h], o[m][n][2 * h + 1]);
+                        if (t == 0) {
+                            part[(size_t)kRows * D + r] = ref[m][h];
+                            part[(size_t)kRows * (D + 1) + r] = l;
+                        }
+                    }
+                }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(done);
+        }
+    }
+
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 2) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+const void *tiles_kernel(const PagedCache &c, int &bytes) {
+    const bool f16 = (c.flags & BCA_PAGED_FP16) != 0;
+    switch (c.d) {
+        case 24:
+            bytes = TilesSmem<24>::BYTES;
+            return f16 ? (const void *)paged_tiles_kernel<24, __half> : (const void *)paged_tiles_kernel<24, __nv_bfloat16>;
+        case 32:
+            bytes = TilesSmem<32>::BYTES;
+            return f16 ? (const void *)paged_tiles_kernel<32, __half> : (const void *)paged_tiles_kernel<32, __nv_bfloat16>;
+        default:
+            bytes = TilesSmem<48>::BYTES;
+            return f16 ? (const void *)paged_tiles_kernel<48, __half> : (const void *)paged_tiles_kernel<48, __nv_bfloat16>;
+    }
+}
+
+}  // namespace
+
+int prepare_paged_tiles(const PagedCache &c) {
+    int bytes = 0;
+    const void *f = tiles_kernel(c, bytes);
+    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess ? BCA_OK
+                                                                                                      : BCA_ERR_CUDA;
+}
+
+int launch_paged_tiles(const PagedCache &c, const PagedArgs &a, cudaStream_t stream) {
+    int bytes = 0;
+    const void *f = tiles_kernel(c, bytes);
+    PagedArgs args = a;
+    void *params[] = {&args};
+    return cudaLaunchKernel(f, dim3((unsigned)a.shares), dim3(kThreads), params, (size_t)bytes, stream) == cudaSuccess
+               ? BCA_OK
+               : BCA_ERR_CUDA;
+}
+
+}  // namespace bca
