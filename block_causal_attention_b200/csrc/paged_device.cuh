@@ -289,6 +289,9 @@ struct Io<__nv_bfloat16> {
     static constexpr bool kF16 = false;
     // P = 2^(s - reference) in bf16 has fp32's exponents: no shift is needed
     static constexpr float kShift = 0.f;
+    // sums of weights may reach this before the reference moves: far below fp32's 2^128, with
+    // room for the values and for 2^31 keys
+    static constexpr float kTop = 1.15292150460684698e18f;  // 2^60
     static __device__ __forceinline__ float2 unpack(uint32_t u) {
         return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u));
     }
@@ -302,6 +305,7 @@ struct Io<__half> {
     // smallest) and 2^6, up to 2^14 before the reference moves, below fp16's 65504; without
     // it a key 2^-14 below the largest would already lose bits of its P.
     static constexpr float kShift = 6.f;
+    static constexpr float kTop = 32768.f;  // no weight above 2^15, below fp16's 65504
     static __device__ __forceinline__ float2 unpack(uint32_t u) {
         return __half22float2(*reinterpret_cast<const __half2 *>(&u));
     }

@@ -79,13 +79,13 @@ __device__ __forceinline__ bool clear_unseen(uint32_t (&vf)[NV][2], int32_t key,
     return __any_sync(0xffffffffu, odd);
 }
 
-// o += p v over the values that clear_unseen left out, for the rows that see their token: p0,
-// p1 the weights of tokens 0 .. 7 and 8 .. 15 in accumulator layout, v the two token groups in
-// shared memory, lim where the lane's two rows' keys end.  Rare, so written for size; inlined, since
-// arrays handed to a function that is not live in memory.
+// o += p v over the values that clear_unseen left out, for the rows that see their token: p the
+// weights as A operand, v the two token groups in shared memory, lim where the lane's two rows'
+// keys end.  Rare, so written for size; inlined, since arrays handed to a function that is not
+// live in memory.
 template <int D, typename T, int NV>
-__device__ __forceinline__ void add_left_out(float (&o)[NV][4], const float (&p0)[4], const float (&p1)[4], const T *v,
-                                          int32_t key0, int32_t kb, const int32_t (&lim)[2]) {
+__device__ __forceinline__ void add_left_out(float (&o)[NV][4], const uint32_t (&p)[4], const T *v, int32_t key0,
+                                             int32_t kb, const int32_t (&lim)[2]) {
     const int lane = threadIdx.x & 31, t = lane & 3;
 #pragma unroll 1
     for (int x = 0; x < 16; ++x) {
@@ -93,9 +93,8 @@ __device__ __forceinline__ void add_left_out(float (&o)[NV][4], const float (&p0
         float w[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            const float even = __shfl_sync(0xffffffffu, x < 8 ? p0[2 * h] : p1[2 * h], src);
-            const float odd = __shfl_sync(0xffffffffu, x < 8 ? p0[2 * h + 1] : p1[2 * h + 1], src);
-            w[h] = x % 2 ? odd : even;
+            const float2 both = Io<T>::unpack(__shfl_sync(0xffffffffu, x < 8 ? p[h] : p[2 + h], src));
+            w[h] = x % 2 ? both.y : both.x;
         }
         const int32_t key = key0 + x;
 #pragma unroll
@@ -107,6 +106,26 @@ __device__ __forceinline__ void add_left_out(float (&o)[NV][4], const float (&p0
                     o[n][j] += w[j >> 1] * (float)y;
             }
     }
+}
+
+// Two fp32 operations in one instruction.
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, c, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+        "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 a, b, d;\n\t"
+        "mov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+        "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
 }
 
 }  // namespace bca

@@ -253,7 +253,7 @@ ldsm_v<NV>(vs + vaddr, vf);
 #pragma unroll
                     for (int n = 0; n < NV; ++n) mma16<Io<T>::kF16>(o[m][n], pa, vf[n][0], vf[n][1]);
                     if (odd)
-                        add_left_out<D, T, NV>(o[m], s[0], s[1],
+                        add_left_out<D, T, NV>(o[m], pa,
                                                reinterpret_cast<const T *>(smem + (vs - sbase)) + 2 * warp * D * 8, key0,
                                                kb, lim[m]);
                 }

@@ -257,6 +257,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
             const int32_t lim_all = x.limit(min(wr, x.left - 1), a.group);
             const int32_t lim_any = x.limit(min(wr + 31, x.left - 1), a.group);
             const int32_t kb = x.kb;
+            bool settled = false;  // every row of the warp has a reference
             for (int32_t p = p0; p < p1; ++p, ++it, ++mine) {
                 const int st = it % S;
                 if (ok)
@@ -266,31 +267,93 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                 tc_fence_after();
                 const bool on = here[st];
                 const uint32_t vs = sbase + L::OFF_RING + st * L::STAGE + L::KSTAGE;
-#pragma unroll 1
-                for (int step = 0; step < kPage / kChunk; ++step) {
-                    const int32_t key0 = p * kPage + kChunk * step;
-                    const bool work = on && key0 + kChunk > kb && key0 < lim_any;
-                    float s[2][kTiles][4];
-                    if (work) {
-                        tmem_ld_frag(tS + kChunk * step, s[0]);
-                        tmem_ld_frag(tS + (16u << 16) + kChunk * step, s[1]);
-                        tmem_wait_ld();
+                const int32_t page0 = p * kPage;
+                float s[2][kTiles][4];
+                uint32_t pa[2][kTiles / 2][4];  // P of the step as A operands
+                auto load_s = [&](int step) {
+                    tmem_ld_frag(tS + kChunk * step, s[0]);
+                    tmem_ld_frag(tS + (16u << 16) + kChunk * step, s[1]);
+                };
+                auto wait_s = [&] {
+                    tmem_wait_ld();
 #pragma unroll
-                        for (int i = 0; i < 8 * kTiles; ++i)
-                            asm volatile("" : "+f"(s[i / (4 * kTiles)][i / 4 % kTiles][i % 4]));
-                    }
-                    if (step == kPage / kChunk - 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(bar(L::B_S_FREE + slot));
-                    }
-                    if (!work) continue;
-                    const bool inside = key0 >= kb && key0 + kChunk <= lim_all;
-                    if (!inside) {
+                    for (int i = 0; i < 8 * kTiles; ++i)
+                        asm volatile("" : "+f"(s[i / (4 * kTiles)][i / 4 % kTiles][i % 4]));
+                };
+                auto free_s = [&] {
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::B_S_FREE + slot));
+                };
+                // P = 2^(scale s - ref) and its sums of the step
+                auto weights = [&](float2 (&add)[2][2]) {
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float neg = ref[m][h] == -INFINITY ? 0.f : -ref[m][h];
+#pragma unroll
+                            for (int n = 0; n < kTiles; ++n) {
+                                float2 y = fma2(make_float2(s[m][n][2 * h], s[m][n][2 * h + 1]),
+                                                make_float2(a.scale, a.scale), make_float2(neg, neg));
+                                y = make_float2(ex2(y.x), ex2(y.y));
+                                add[m][h] = n == 0 ? y : add2(add[m][h], y);
+                                pa[m][n / 2][2 * (n & 1) + h] = Io<T>::pack(y.x, y.y);
+                            }
+                        }
+                };
+                int step = 0;
+                if (on && settled && page0 >= kb && page0 + kPage <= lim_all) {
+                    // Every row sees the whole page.  The maxima are not looked at: weights may grow
+                    // to kTop before the reference has to move, and their sums, which are needed
+                    // anyway, tell.
+                    load_s(0);
+#pragma unroll
+                    for (; step < kPage / kChunk; ++step) {
+                        wait_s();
+                        float2 add[2][2];
+                        weights(add);
+                        bool high = false;
 #pragma unroll
                         for (int m = 0; m < 2; ++m)
 #pragma unroll
-                            for (int h = 0; h < 2; ++h) {
+                            for (int h = 0; h < 2; ++h) high |= add[m][h].x + add[m][h].y > Io<T>::kTop;
+                        if (__any_sync(0xffffffffu, high)) break;
+                        if (step + 1 < kPage / kChunk) load_s(step + 1);
+                        else free_s();
+#pragma unroll
+                        for (int m = 0; m < 2; ++m)
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) sum[m][h] += add[m][h].x + add[m][h].y;
+#pragma unroll
+                        for (int k = 0; k < kChunk / 16; ++k) {
+                            uint32_t vf[NV][2];
+                            ldsm_v<NV>(vs + (step * kTiles + 2 * k) * (D * 16) + vaddr, vf);
+#pragma unroll
+                            for (int m = 0; m < 2; ++m)
+#pragma unroll
+                                for (int n = 0; n < NV; ++n) mma16<Io<T>::kF16>(o[m][n], pa[m][k], vf[n][0], vf[n][1]);
+                        }
+                    }
+                }
+                // Else, or from the step on that passed kTop: with masks and the running maximum.
+#pragma unroll 1
+                for (; step < kPage / kChunk; ++step) {
+                    const int32_t key0 = page0 + kChunk * step;
+                    const bool work = on && key0 + kChunk > kb && key0 < lim_any;
+                    if (work) {
+                        load_s(step);
+                        wait_s();
+                    }
+                    if (step == kPage / kChunk - 1) free_s();
+                    if (!work) continue;
+                    const bool inside = key0 >= kb && key0 + kChunk <= lim_all;
+                    settled = true;
+#pragma unroll
+                    for (int m = 0; m < 2; ++m)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            if (!inside) {
                                 const int32_t lim = x.limit(wr + 16 * m + 8 * h + g, a.group);
 #pragma unroll
                                 for (int n = 0; n < kTiles; ++n)
@@ -300,82 +363,49 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                                         if (key < kb || key >= lim) s[m][n][2 * h + j] = -INFINITY;
                                     }
                             }
-                    }
-                    float mx[2][2];
-                    bool grow = false;
-#pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
                             float top = s[m][0][2 * h];
 #pragma unroll
-                            for (int n = 0; n < kTiles; ++n) {
-                                top = fmaxf(top, s[m][n][2 * h]);
-                                top = fmaxf(top, s[m][n][2 * h + 1]);
-                            }
-                            mx[m][h] = top * a.scale;
-                            grow |= mx[m][h] > ref[m][h] + (kShift + kLazy);
-                        }
-                    if (__any_sync(0xffffffffu, grow)) {
+                            for (int n = 0; n < kTiles; ++n) top = fmaxf(top, fmaxf(s[m][n][2 * h], s[m][n][2 * h + 1]));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2)) * a.scale - kShift;
+                            if (top > ref[m][h]) {
+                                const float mul = ref[m][h] == -INFINITY ? 0.f : ex2(ref[m][h] - top);
+                                ref[m][h] = top;
+                                sum[m][h] *= mul;
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                float top = mx[m][h];
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
-                                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                                if (top > ref[m][h] + (kShift + kLazy)) {
-                                    const float now = top - kShift;
-                                    const float mul = ref[m][h] == -INFINITY ? 0.f : ex2(ref[m][h] - now);
-                                    ref[m][h] = now;
-                                    sum[m][h] *= mul;
-#pragma unroll
-                                    for (int n = 0; n < NV; ++n) {
-                                        o[m][n][2 * h] *= mul;
-                                        o[m][n][2 * h + 1] *= mul;
-                                    }
+                                for (int n = 0; n < NV; ++n) {
+                                    o[m][n][2 * h] *= mul;
+                                    o[m][n][2 * h + 1] *= mul;
                                 }
                             }
-                    }
-                    float sub[2][2];
+                            settled &= ref[m][h] != -INFINITY;
+                        }
+                    settled = __all_sync(0xffffffffu, settled);
+                    float2 add[2][2];
+                    weights(add);
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) sub[m][h] = ref[m][h] == -INFINITY ? 0.f : -ref[m][h];
+                        for (int h = 0; h < 2; ++h) sum[m][h] += add[m][h].x + add[m][h].y;
 #pragma unroll
                     for (int k = 0; k < kChunk / 16; ++k) {
-                        uint32_t pa[2][4];
-#pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int b = 0; b < 2; ++b)
-#pragma unroll
-                                for (int h = 0; h < 2; ++h) {
-                                    float *y = &s[m][2 * k + b][2 * h];
-                                    y[0] = ex2(fmaf(y[0], a.scale, sub[m][h]));
-                                    y[1] = ex2(fmaf(y[1], a.scale, sub[m][h]));
-                                    sum[m][h] += y[0];
-                                    sum[m][h] += y[1];
-                                    pa[m][2 * b + h] = Io<T>::pack(y[0], y[1]);
-                                }
-                        const uint32_t va = vs + (step * kTiles + 2 * k) * (D * 16) + vaddr;
-                        uint32_t vf[NV][2];
-                        ldsm_v<NV>(va, vf);
-                        bool odd = false;
+                        const uint32_t at = (step * kTiles + 2 * k) * (D * 16);
                         const int32_t keyk = key0 + 16 * k;
+                        uint32_t vf[NV][2];
+                        ldsm_v<NV>(vs + at + vaddr, vf);
+                        bool odd = false;
                         if (!inside) odd = clear_unseen<T, NV>(vf, keyk + 2 * t, kb, lim_any);
 #pragma unroll
-                        for (int m = 0; m < 2; ++m)
+                        for (int m = 0; m < 2; ++m) {
 #pragma unroll
-                            for (int n = 0; n < NV; ++n) mma16<Io<T>::kF16>(o[m][n], pa[m], vf[n][0], vf[n][1]);
-                        if (odd) {
-                            const T *v = reinterpret_cast<const T *>(smem + (vs - sbase)) + (step * kTiles + 2 * k) * D * 8;
-#pragma unroll
-                            for (int m = 0; m < 2; ++m) {
+                            for (int n = 0; n < NV; ++n) mma16<Io<T>::kF16>(o[m][n], pa[m][k], vf[n][0], vf[n][1]);
+                            if (odd) {
                                 int32_t lim[2];
 #pragma unroll
                                 for (int h = 0; h < 2; ++h) lim[h] = x.limit(wr + 16 * m + 8 * h + g, a.group);
-                                add_left_out<D, T, NV>(o[m], s[m][2 * k], s[m][2 * k + 1], v, keyk, kb, lim);
+                                add_left_out<D, T, NV>(o[m], pa[m][k],
+                                                       reinterpret_cast<const T *>(smem + (vs + at - sbase)), keyk, kb,
+                                                       lim);
                             }
                         }
                     }
