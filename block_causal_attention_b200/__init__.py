@@ -250,4 +250,9 @@ class Plan:
             pass
 
 
-from .paged import PagedCache, PagePool  # noqa: E402,F401
+def __getattr__(name):
+    # on first use: the module needs PyTorch, which the host side of a plan does not
+    if name in ("PagedCache", "PagePool"):
+        from . import paged
+        return getattr(paged, name)
+    raise AttributeError(f"module {__name__!r} has no attribute {name!r}")

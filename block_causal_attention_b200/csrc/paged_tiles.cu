@@ -27,6 +27,7 @@ using namespace sm100;
 namespace {
 
 constexpr int kSlots = 3;                  // 128-row tiles that share a page
+constexpr int kBuffers = 4;                // S tiles of 128 x 128 in tensor memory, used in turn
 constexpr int kRows = kPagedTileRows;
 constexpr int kThreads = 128 + 128 * kSlots;
 static_assert(kRows == 128 * kSlots, "rows of a work item");
@@ -46,8 +47,8 @@ struct TilesSmem {
     static constexpr int B_EMPTY = STAGES;
     static constexpr int B_ITEM = 2 * STAGES;
     static constexpr int B_S_FULL = B_ITEM + 2 * kItemRing;
-    static constexpr int B_S_FREE = B_S_FULL + kSlots;
-    static constexpr int B_Q = B_S_FREE + kSlots;
+    static constexpr int B_S_FREE = B_S_FULL + kSlots * kBuffers;  // full: of a slot's use of a buffer
+    static constexpr int B_Q = B_S_FREE + kBuffers;
     static constexpr int B_DONE = B_Q + kSlots;
     static constexpr int OFF_HERE = OFF_BAR + 8 * (B_DONE + 1);
     static constexpr int OFF_TMEM = OFF_HERE + 4 * STAGES;
@@ -104,11 +105,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
             mbar_init(bar(L::B_FULL + i), 1);
             mbar_init(bar(L::B_EMPTY + i), 4 * kSlots);
         }
-        for (int s = 0; s < kSlots; ++s) {
-            mbar_init(bar(L::B_S_FULL + s), 1);
-            mbar_init(bar(L::B_S_FREE + s), 4);
-            mbar_init(bar(L::B_Q + s), 4);
-        }
+        for (int i = 0; i < kSlots * kBuffers; ++i) mbar_init(bar(L::B_S_FULL + i), 1);
+        for (int i = 0; i < kBuffers; ++i) mbar_init(bar(L::B_S_FREE + i), 4);
+        for (int s = 0; s < kSlots; ++s) mbar_init(bar(L::B_Q + s), 4);
         for (int i = 0; i < kItemRing; ++i) {
             mbar_init(bar(L::B_ITEM + i), 1);
             mbar_init(bar(L::B_ITEM + kItemRing + i), 1 + 4 * kSlots);
@@ -145,7 +144,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
         // ------------------------------------------------ S = Q K^T
         if (lane == 0) {
             int it = 0;
-            int queries[kSlots] = {}, count[kSlots] = {};  // of each slot: query tiles and S tiles so far
+            int queries[kSlots] = {};  // query tiles of each slot so far
+            uint32_t made = 0;         // S tiles so far
             bool ok = true;
             for (int n = 0; ok; ++n) {
                 ok = paged_wait(bar(L::B_ITEM + n % kItemRing), (n / kItemRing) & 1, a, abort_flag);
@@ -164,18 +164,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
 #pragma unroll
                     for (int s = 0; s < kSlots; ++s) {
                         if (!ok || s * 128 >= left) continue;
-                        if (count[s] > 0)
-                            ok = paged_wait(bar(L::B_S_FREE + s), (count[s] - 1) & 1, a, abort_flag);
+                        const uint32_t buf = made % kBuffers;
+                        if (made >= kBuffers)
+                            ok = paged_wait(bar(L::B_S_FREE + buf), (made / kBuffers - 1) & 1, a, abort_flag);
                         if (!ok) continue;
-                        ++count[s];
+                        ++made;
                         tc_fence_after();
                         const uint32_t qa = sbase + L::OFF_Q + s * L::Q_BYTES;
                         const uint32_t kb = sbase + L::OFF_RING + st * L::STAGE;
 #pragma unroll
                         for (int k = 0; k < L::DPAD / 16; ++k)
-                            mma_f16(tbase + 128 * s, smem_desc(qa + k * 4096, 2048, 128),
+                            mma_f16(tbase + 128 * buf, smem_desc(qa + k * 4096, 2048, 128),
                                     smem_desc(kb + k * 4096, 2048, 128), IDESC, k > 0);
-                        mma_commit(bar(L::B_S_FULL + s));
+                        mma_commit(bar(L::B_S_FULL + s * kBuffers + buf));
                     }
                 }
             }
@@ -194,10 +195,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
         // ------------------------------------------------ softmax and O += P V
         const int slot = (warp - 4) >> 2, quarter = warp & 3;
         const int g = lane >> 2, t = lane & 3;
-        const uint32_t tS = tbase + ((uint32_t)(quarter * 32) << 16) + 128 * slot;
+        const uint32_t tlane = tbase + ((uint32_t)(quarter * 32) << 16);
         // rows 8 j .. of matrix j: V's token group j % 2, channel group j / 2
         const uint32_t vaddr = ((lane >> 3 & 1) * D + 8 * (lane >> 4) + (lane & 7)) * 16;
-        int it = 0, mine = 0;
+        int it = 0;
+        uint32_t made = 0;                         // S tiles before this item
+        // Parity of the next use of each buffer by this slot.  The slots take turns with the
+        // buffers, so a barrier of a buffer alone would run through phases that this warp does not
+        // wait for, and its parity would tell it nothing.
+        uint32_t parity = 0;
         bool ok = true;
         const int wr = slot * 128 + quarter * 32;  // the warp's first row of the work tile
         for (int n_item = 0; ok; ++n_item) {
@@ -208,11 +214,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
             const PagedItem &x = items[n_item % kItemRing];
             const int32_t p0 = x.p0, p1 = x.p1;
             if (p0 < 0) break;
+            const int active = (x.left + 127) / 128;  // slots that have rows
             if (slot * 128 >= x.left) {
                 for (int32_t p = p0; p < p1 && ok; ++p, ++it) {
                     ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_FULL + it % S), (it / S) & 1, a, abort_flag));
                     if (ok && lane == 0) mbar_arrive(bar(L::B_EMPTY + it % S));
                 }
+                made += (p1 - p0) * active;
                 __syncwarp();
                 if (lane == 0) mbar_arrive(done);
                 continue;
@@ -258,94 +266,173 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
             const int32_t lim_any = x.limit(min(wr + 31, x.left - 1), a.group);
             const int32_t kb = x.kb;
             bool settled = false;  // every row of the warp has a reference
-            for (int32_t p = p0; p < p1; ++p, ++it, ++mine) {
-                const int st = it % S;
+            uint32_t tile = made + slot;   // this warp's S tile: buffer tile % kBuffers
+            made += (p1 - p0) * active;
+            float s[2][kTiles][4];
+            uint32_t pa[2][kTiles / 2][4];  // P of a step as A operands: [16-row tile][16 keys]
+            auto load_s = [&](int step) {
+                const uint32_t at = tlane + 128 * (tile % kBuffers) + kChunk * step;
+                tmem_ld_frag(at, s[0]);
+                tmem_ld_frag(at + (16u << 16), s[1]);
+            };
+            auto wait_s = [&] {
+                tmem_wait_ld();
+#pragma unroll
+                for (int i = 0; i < 8 * kTiles; ++i)
+                    asm volatile("" : "+f"(s[i / (4 * kTiles)][i / 4 % kTiles][i % 4]));
+            };
+            auto free_s = [&] {
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_S_FREE + tile % kBuffers));
+            };
+            auto free_page = [&](int st) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_EMPTY + st));
+            };
+            // Keys and values of page `it` and the warp's S of them.
+            auto wait_page = [&] {
+                const uint32_t buf = tile % kBuffers;
                 if (ok)
-                    ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_FULL + st), (it / S) & 1, a, abort_flag) &&
-                                                     paged_wait(bar(L::B_S_FULL + slot), mine & 1, a, abort_flag));
-                if (!ok) break;
+                    ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_FULL + it % S), (it / S) & 1, a, abort_flag) &&
+                                                     paged_wait(bar(L::B_S_FULL + slot * kBuffers + buf),
+                                                                parity >> buf & 1, a, abort_flag));
+                parity ^= 1u << buf;
                 tc_fence_after();
-                const bool on = here[st];
-                const uint32_t vs = sbase + L::OFF_RING + st * L::STAGE + L::KSTAGE;
-                const int32_t page0 = p * kPage;
-                float s[2][kTiles][4];
-                uint32_t pa[2][kTiles / 2][4];  // P of the step as A operands
-                auto load_s = [&](int step) {
-                    tmem_ld_frag(tS + kChunk * step, s[0]);
-                    tmem_ld_frag(tS + (16u << 16) + kChunk * step, s[1]);
-                };
-                auto wait_s = [&] {
-                    tmem_wait_ld();
+                return ok;
+            };
+            auto page_v = [&](int st) { return sbase + L::OFF_RING + st * L::STAGE + L::KSTAGE; };
+            // P = 2^(scale s - ref) of 16 rows x 16 keys, and the sums
+            auto weights = [&](int m, int k, uint32_t (&to)[4], float2 (&add)[2]) {
 #pragma unroll
-                    for (int i = 0; i < 8 * kTiles; ++i)
-                        asm volatile("" : "+f"(s[i / (4 * kTiles)][i / 4 % kTiles][i % 4]));
-                };
-                auto free_s = [&] {
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(bar(L::B_S_FREE + slot));
-                };
-                // P = 2^(scale s - ref) and its sums of the step
-                auto weights = [&](float2 (&add)[2][2]) {
+                for (int h = 0; h < 2; ++h) {
+                    const float neg = ref[m][h] == -INFINITY ? 0.f : -ref[m][h];
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float neg = ref[m][h] == -INFINITY ? 0.f : -ref[m][h];
-#pragma unroll
-                            for (int n = 0; n < kTiles; ++n) {
-                                float2 y = fma2(make_float2(s[m][n][2 * h], s[m][n][2 * h + 1]),
-                                                make_float2(a.scale, a.scale), make_float2(neg, neg));
-                                y = make_float2(ex2(y.x), ex2(y.y));
-                                add[m][h] = n == 0 ? y : add2(add[m][h], y);
-                                pa[m][n / 2][2 * (n & 1) + h] = Io<T>::pack(y.x, y.y);
-                            }
-                        }
-                };
-                int step = 0;
-                if (on && settled && page0 >= kb && page0 + kPage <= lim_all) {
-                    // Every row sees the whole page.  The maxima are not looked at: weights may grow
-                    // to kTop before the reference has to move, and their sums, which are needed
-                    // anyway, tell.
-                    load_s(0);
-#pragma unroll
-                    for (; step < kPage / kChunk; ++step) {
-                        wait_s();
-                        float2 add[2][2];
-                        weights(add);
-                        bool high = false;
-#pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) high |= add[m][h].x + add[m][h].y > Io<T>::kTop;
-                        if (__any_sync(0xffffffffu, high)) break;
-                        if (step + 1 < kPage / kChunk) load_s(step + 1);
-                        else free_s();
-#pragma unroll
-                        for (int m = 0; m < 2; ++m)
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) sum[m][h] += add[m][h].x + add[m][h].y;
-#pragma unroll
-                        for (int k = 0; k < kChunk / 16; ++k) {
-                            uint32_t vf[NV][2];
-                            ldsm_v<NV>(vs + (step * kTiles + 2 * k) * (D * 16) + vaddr, vf);
-#pragma unroll
-                            for (int m = 0; m < 2; ++m)
-#pragma unroll
-                                for (int n = 0; n < NV; ++n) mma16<Io<T>::kF16>(o[m][n], pa[m][k], vf[n][0], vf[n][1]);
-                        }
+                    for (int b = 0; b < 2; ++b) {
+                        const float *x = &s[m][2 * k + b][2 * h];
+                        float2 y = fma2(make_float2(x[0], x[1]), make_float2(a.scale, a.scale), make_float2(neg, neg));
+                        y = make_float2(ex2(y.x), ex2(y.y));
+                        add[h] = b == 0 && k == 0 ? y : add2(add[h], y);
+                        to[2 * b + h] = Io<T>::pack(y.x, y.y);
                     }
                 }
+            };
+            // A step in which every row sees every key.  The maxima are not looked at: weights may
+            // grow to kTop before the reference has to move, and their sums, which are needed
+            // anyway, tell.  Half of the step before's P V products stand between its exponentials
+            // (the other half has covered the way of its scores from tensor memory), so that a warp
+            // alone keeps both units at work.  False, with s still to be had from tensor
+            // memory, if the reference has to move.
+            auto fast_step = [&](bool before, uint32_t vs, int vstep) {
+                uint32_t pn[2][kTiles / 2][4];
+                float2 add[2][2];
+                uint32_t vf[NV][2];
+                if (before) ldsm_v<NV>(vs + (vstep * kTiles + 2) * (D * 16) + vaddr, vf);
+#pragma unroll
+                for (int k = 0; k < kChunk / 16; ++k)
+#pragma unroll
+                    for (int m = 0; m < 2; ++m) {
+                        weights(m, k, pn[m][k], add[m]);
+                        if (before)
+#pragma unroll
+                            for (int n = k * NV / 2; n < (k + 1) * NV / 2; ++n)
+                                mma16<Io<T>::kF16>(o[m][n], pa[m][1], vf[n][0], vf[n][1]);
+                    }
+                bool high = false;
+                float row[2][2];
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        row[m][h] = add[m][h].x + add[m][h].y;
+                        high |= row[m][h] > Io<T>::kTop;
+                    }
+                if (__any_sync(0xffffffffu, high)) return false;
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) sum[m][h] += row[m][h];
+#pragma unroll
+                    for (int k = 0; k < kChunk / 16; ++k)
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) pa[m][k][j] = pn[m][k][j];
+                }
+                return true;
+            };
+            auto products = [&](uint32_t vs, int vstep, int k) {  // the 16 keys k of a step
+                uint32_t vf[NV][2];
+                ldsm_v<NV>(vs + (vstep * kTiles + 2 * k) * (D * 16) + vaddr, vf);
+#pragma unroll
+                for (int m = 0; m < 2; ++m)
+#pragma unroll
+                    for (int n = 0; n < NV; ++n) mma16<Io<T>::kF16>(o[m][n], pa[m][k], vf[n][0], vf[n][1]);
+            };
+            constexpr int kSteps = kPage / kChunk;
+
+            for (int32_t p = p0; p < p1; ++p, ++it, tile += active) {
+                if (!wait_page()) break;
+                int32_t page0 = p * kPage;
+                bool on = here[it % S];
+                int step = 0;
+                if (on && settled && page0 >= kb && page0 + kPage <= lim_all) {
+                    load_s(0);
+                    wait_s();
+                    if (fast_step(false, 0, 0)) {
+                        // the products of step - 1 are still to be made
+                        for (;;) {
+                            const uint32_t vs = page_v(it % S);
+                            load_s(1);
+                            products(vs, 0, 0);
+#pragma unroll
+                            for (step = 1; step < kSteps; ++step) {
+                                wait_s();
+                                if (!fast_step(true, vs, step - 1)) break;
+                                if (step + 1 < kSteps) {
+                                    load_s(step + 1);
+                                    products(vs, step, 0);
+                                } else {
+                                    free_s();
+                                }
+                            }
+                            if (step < kSteps) break;
+                            // on to the next page, if that one is seen whole too
+                            if (p + 1 >= p1 || page0 + 2 * kPage > lim_all) {
+                                products(vs, kSteps - 1, 0);
+                                products(vs, kSteps - 1, 1);
+                                break;
+                            }
+                            const int old = it % S;
+                            ++p, ++it, tile += active;
+                            page0 += kPage;
+                            if (!wait_page()) break;
+                            on = here[it % S];
+                            step = 0;
+                            if (on) load_s(0);
+                            products(vs, kSteps - 1, 0);
+                            if (!on) {
+                                products(vs, kSteps - 1, 1);
+                                free_page(old);
+                                break;
+                            }
+                            wait_s();
+                            const bool go = fast_step(true, vs, kSteps - 1);
+                            free_page(old);
+                            if (!go) break;
+                        }
+                        if (!ok) break;
+                    }
+                }
+                const uint32_t vs = page_v(it % S);
                 // Else, or from the step on that passed kTop: with masks and the running maximum.
 #pragma unroll 1
-                for (; step < kPage / kChunk; ++step) {
+                for (; step < kSteps; ++step) {
                     const int32_t key0 = page0 + kChunk * step;
                     const bool work = on && key0 + kChunk > kb && key0 < lim_any;
                     if (work) {
                         load_s(step);
                         wait_s();
                     }
-                    if (step == kPage / kChunk - 1) free_s();
+                    if (step == kSteps - 1) free_s();
                     if (!work) continue;
                     const bool inside = key0 >= kb && key0 + kChunk <= lim_all;
                     settled = true;
@@ -381,12 +468,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                             settled &= ref[m][h] != -INFINITY;
                         }
                     settled = __all_sync(0xffffffffu, settled);
-                    float2 add[2][2];
-                    weights(add);
 #pragma unroll
-                    for (int m = 0; m < 2; ++m)
+                    for (int m = 0; m < 2; ++m) {
+                        float2 add[2];
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) sum[m][h] += add[m][h].x + add[m][h].y;
+                        for (int k = 0; k < kChunk / 16; ++k) weights(m, k, pa[m][k], add);
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) sum[m][h] += add[h].x + add[h].y;
+                    }
 #pragma unroll
                     for (int k = 0; k < kChunk / 16; ++k) {
                         const uint32_t at = (step * kTiles + 2 * k) * (D * 16);
@@ -410,8 +499,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                         }
                     }
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::B_EMPTY + st));
+                free_page(it % S);
             }
 
             // ------------------------------------------------ O / l and the LSE, or this block's piece

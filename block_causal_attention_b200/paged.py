@@ -12,6 +12,7 @@ import heapq
 from typing import Dict, List, Optional, Sequence
 
 import numpy as np
+import torch
 
 from . import _abi
 
@@ -29,7 +30,6 @@ class PagedCache:
     def __init__(self, hq: int, hkv: int, d: int, pages: int, *, layers: int = 1, dtype=None,
                  rope_base=(1e4, 1e4, 1e4), eps: float = 1e-6, o_fp32: bool = False, k_pages=None, v_pages=None,
                  host_only: bool = False, test_force_timeout: bool = False):
-        import torch
         dtype = torch.bfloat16 if dtype is None else dtype
         if dtype not in (torch.bfloat16, torch.float16):
             raise ValueError(f"dtype: expected torch.bfloat16 or torch.float16, got {dtype}")
@@ -50,7 +50,9 @@ class PagedCache:
         self.k_shape = (self.layers, self.pages, self.hkv, self.d // 8, PAGE, 8)
         self.v_shape = (self.layers, self.pages, self.hkv, PAGE // 8, self.d, 8)
         self.pool_bytes = int(self._lib.bca_paged_pool_bytes(self._h))
-        self.k_pages = self.v_pages = self.device = None
+        self._pools: Dict[str, torch.Tensor] = {}
+        self.device = None
+        self._o_dtype = torch.float32 if self.o_fp32 else dtype
         if self.host_only:
             return
         self.device = torch.device("cuda", torch.cuda.current_device())
@@ -60,20 +62,34 @@ class PagedCache:
                 t = torch.empty(shape, dtype=dt, device=self.device)
             else:
                 self._tensor(name, t, dt, shape)
-            setattr(self, name, t)
+            self._pools[name] = t
+        self._index = self.device.index
+        self._k_pool, self._v_pool = self.k_pages.data_ptr(), self.v_pages.data_ptr()
+
+    @property
+    def k_pages(self):
+        """[layers][pages][Hkv][D/8][128][8] fp16 (None in a host-only cache)."""
+        return self._pools.get("k_pages")
+
+    @property
+    def v_pages(self):
+        """[layers][pages][Hkv][16][D][8], the cache's dtype."""
+        return self._pools.get("v_pages")
 
     # ------------------------------------------------------------------ arguments
+    # These run before every launch, so they are written for few interpreter steps.
     def _tensor(self, name, t, dtype, shape):
-        if t.dtype != dtype or t.device != self.device or tuple(t.shape) != shape or not t.is_contiguous():
-            raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {self.device}, got "
-                             f"{t.dtype} {tuple(t.shape)} on {t.device}")
-        return t.data_ptr()
+        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == self.device:
+            return t.data_ptr()
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {self.device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
 
     def _prologue(self, rows, pos, gain, gain_name):
-        import torch
-        if pos is None and gain is not None:
-            raise ValueError(f"{gain_name} needs pos: rows without positions are taken as post-prologue")
-        return (None if pos is None else self._tensor("pos", pos, torch.int32, (rows, 3)),
+        if pos is None:
+            if gain is not None:
+                raise ValueError(f"{gain_name} needs pos: rows without positions are taken as post-prologue")
+            return None, None
+        return (self._tensor("pos", pos, torch.int32, (rows, 3)),
                 None if gain is None else self._tensor(gain_name, gain, torch.float32, (self.d,)))
 
     def _layer(self, layer):
@@ -82,18 +98,17 @@ class PagedCache:
         if not 0 <= layer < self.layers:
             raise ValueError(f"layer {layer} of {self.layers}")
         at = layer * self.pool_bytes
-        return self.k_pages.data_ptr() + at, self.v_pages.data_ptr() + at
+        return self._k_pool + at, self._v_pool + at
 
     def _table(self, table):
-        import torch
-        if table.dim() != 2:
+        shape = table.shape
+        if len(shape) != 2:
             raise ValueError("table: expected int32 [seqs, width]")
-        return self._tensor("table", table, torch.int32, tuple(table.shape)), table.shape[0], table.shape[1]
+        return self._tensor("table", table, torch.int32, shape), shape[0], shape[1]
 
     def _stream(self, stream):
-        import torch
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
+            return torch.cuda.current_stream(self._index).cuda_stream
         return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else stream
 
     # ------------------------------------------------------------------ operators
@@ -103,7 +118,6 @@ class PagedCache:
         through QK-Norm (k_gain, or ones) and RoPE; without, they are given post-prologue.
         table, off, start, pos: int32 tensors on the cache's device, read when the kernel runs.
         A token that has no page is dropped and reported by ``status``."""
-        import torch
         kp, vp = self._layer(layer)
         n = k.shape[0]
         shape = (n, self.hkv, self.d)
@@ -146,26 +160,27 @@ class PagedCache:
 
         Returns o; rows that see no key are zero.  Rows outside every slice are left as they
         were in a given o (else uninitialised).  lse (fp32 [Hq, nq], optional) is filled in."""
-        import torch
         kp, vp = self._layer(layer)
         nq = q.shape[0]
         qp = self._tensor("q", q, self.dtype, (nq, self.hq, self.d))
         tab, seqs, width = self._table(table)
-        slices = off.shape[0] - 1 if off.dim() == 1 else -1
-        if slices < 0:
+        shape = off.shape
+        if len(shape) != 1 or shape[0] < 1:
             raise ValueError("off: expected int32 [slices + 1]")
+        slices = shape[0] - 1
         i32, per_slice = torch.int32, (slices,)
-        offp = self._tensor("off", off, i32, (slices + 1,))
+        offp = self._tensor("off", off, i32, shape)
         if seq is None and slices != seqs:
             raise ValueError("seq=None needs as many slices as table rows")
         sp = None if seq is None else self._tensor("seq", seq, i32, per_slice)
         kb = self._tensor("k_begin", k_begin, i32, per_slice)
         ke = self._tensor("k_end", k_end, i32, per_slice)
         p, gain = self._prologue(nq, pos, q_gain, "q_gain")
-        odt = torch.float32 if self.o_fp32 else self.dtype
         if o is None:
-            o = torch.empty((nq, self.hq, self.d), dtype=odt, device=self.device)
-        op = self._tensor("o", o, odt, (nq, self.hq, self.d))
+            o = torch.empty((nq, self.hq, self.d), dtype=self._o_dtype, device=self.device)
+            op = o.data_ptr()
+        else:
+            op = self._tensor("o", o, self._o_dtype, (nq, self.hq, self.d))
         lp = None if lse is None else self._tensor("lse", lse, torch.float32, (self.hq, nq))
         if workspace is None:
             workspace = self.alloc_workspace(nq, slices, stream)
@@ -184,7 +199,6 @@ class PagedCache:
     def alloc_workspace(self, nq: int, slices: int, stream=None):
         """Workspace of an ``attend`` call of these sizes, on its stream.  Calls that may overlap
         on the GPU (two streams, two captured graphs replayed side by side) need one each."""
-        import torch
         n = max(16, self.workspace_bytes(nq, slices))
         if stream is None:
             return torch.empty(n, dtype=torch.uint8, device=self.device)
