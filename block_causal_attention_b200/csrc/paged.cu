@@ -231,71 +231,79 @@ int launch_copy(const CopyArgs &a, const PagedCache &c, const int32_t *pairs, in
 //
 // O = sum_p 2^(r_p - r) O_p / sum_p 2^(r_p - r) l_p with r the largest reference, over the
 // pieces p of an item, always in the order of the blocks that made them.  Block c joins the
-// item that share c begins and does not end.  Eight lanes a piece and row, four pieces of a
-// row at a time.
+// item that share c begins and does not end.  A warp takes a row: first its pieces' references
+// and sums, a lane each, then O, eight lanes a piece, with the loads of 32 pieces on the way
+// at a time: three trips to memory whatever their number up to 32.
 
 constexpr int kJoinThreads = 512;
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a) {
-    __shared__ PagedLocate sh;
-    PagedCursor cur;
-    uint64_t lo, hi, total;
-    const int c = blockIdx.x;
-    const bool found = paged_locate(a, c, true, sh, lo, hi, total, cur);
     asm volatile("griddepcontrol.wait;" ::: "memory");
-    // nothing is cut behind share c, or the item began in an earlier share
-    if (!found || cur.start == hi || cur.start < lo) return;
-    const uint64_t end = cur.end();
+    const int c = blockIdx.x;
+    const PagedJoin j = a.joins[c];
+    const int pieces = j.last - c + 1;
+    if (j.last < c) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / 8, e = lane % 8;
+    const size_t slot = (size_t)a.rows * (D + 2);
     const int rows = a.rows / gridDim.y;
-    for (int row = blockIdx.y * rows + warp; row < (int)(blockIdx.y + 1) * rows; row += kJoinThreads / 32) {
-        const int64_t packed = cur.t * a.rows + row;
-        if (packed / a.group >= cur.s.n) continue;
+    for (int row = blockIdx.y * rows + warp; row < min((int)(blockIdx.y + 1) * rows, j.left); row += kJoinThreads / 32) {
         float ref = -INFINITY, sum = 0.f, o[D / 8] = {};
-        for (int x0 = c; x0 < a.shares; x0 += 4) {
-            const int x = x0 + sub;
-            const uint64_t from = paged_share(total, a.shares, x), to = paged_share(total, a.shares, x + 1);
-            int32_t p0 = 0, p1 = 0;
-            if (x < a.shares && from < end && to > from) cur.pages(a, from, to, p0, p1);
-            if (p0 < p1) {
-                const float *part = paged_part(a, D, 2 * x + (x == c ? 1 : 0));
-                const float r = part[a.rows * D + row], l = part[a.rows * (D + 1) + row];
-                float y[D / 8];
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) y[i] = part[(size_t)row * D + e + 8 * i];
-                const float top = fmaxf(ref, r);
-                const float mul = top == -INFINITY ? 0.f : sm100::ex2(ref - top);
-                const float add = top == -INFINITY ? 0.f : sm100::ex2(r - top);
-                sum = sum * mul + l * add;
-#pragma unroll
-                for (int i = 0; i < D / 8; ++i) o[i] = o[i] * mul + y[i] * add;
-                ref = top;
+        for (int base = 0; base < pieces; base += 32) {
+            const int x = base + lane;
+            const float *part = a.part + (2 * (size_t)(c + x) + (x == 0 ? 1 : 0)) * slot;
+            float r = -INFINITY, l = 0.f;
+            if (x < pieces) {
+                r = part[(size_t)a.rows * D + row];
+                l = part[(size_t)a.rows * (D + 1) + row];
             }
-            if (paged_share(total, a.shares, min(x0 + 4, a.shares)) >= end) break;
-        }
+            float top = r;
 #pragma unroll
-        for (int s = 8; s < 32; s <<= 1) {
-            const float r = __shfl_xor_sync(0xffffffffu, ref, s), l = __shfl_xor_sync(0xffffffffu, sum, s);
-            const float top = fmaxf(ref, r);
-            const float mul = top == -INFINITY ? 0.f : sm100::ex2(ref - top);
-            const float add = top == -INFINITY ? 0.f : sm100::ex2(r - top);
-            sum = sum * mul + l * add;
+            for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
+            top = fmaxf(top, ref);
+            if (top == -INFINITY) continue;
+            const float keep = ref == -INFINITY ? 0.f : sm100::ex2(ref - top);
+            const float w = r == -INFINITY ? 0.f : sm100::ex2(r - top);
+            l *= w;
 #pragma unroll
-            for (int i = 0; i < D / 8; ++i) o[i] = o[i] * mul + __shfl_xor_sync(0xffffffffu, o[i], s) * add;
+            for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
+            sum = sum * keep + l;
             ref = top;
+            float y[8][D / 8];
+            const float *first = a.part + (size_t)row * D + e;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const int z = base + 4 * i + sub;
+                const bool on = __shfl_sync(0xffffffffu, r, 4 * i + sub) != -INFINITY && z < pieces;
+                const float *from = first + (2 * (size_t)(c + z) + (z == 0 ? 1 : 0)) * slot;
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) y[i][k] = on ? from[8 * k] : 0.f;
+            }
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) o[k] *= keep;
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const float m = __shfl_sync(0xffffffffu, w, 4 * i + sub);
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) o[k] = fmaf(y[i][k], m, o[k]);
+            }
         }
+#pragma unroll
+        for (int s = 8; s < 32; s <<= 1)
+#pragma unroll
+            for (int k = 0; k < D / 8; ++k) o[k] += __shfl_xor_sync(0xffffffffu, o[k], s);
         if (sub != 0) continue;
         const bool none = ref == -INFINITY;
         const float inv = none ? 0.f : 1.f / sum;
-        const int64_t token = cur.s.r0 + packed / a.group;
-        const int head = cur.g * a.group + (int)(packed % a.group);
+        const uint32_t packed = j.head + row;
+        const int64_t token = j.row + j.token + (int32_t)(packed / a.group);
+        const int head = j.g * a.group + (int)(packed % a.group);
         const int64_t at = (token * a.hq + head) * D;
 #pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            const float y = none ? 0.f : o[i] * inv;
-            if (a.o_fp32) static_cast<float *>(a.o)[at + e + 8 * i] = y;
-            else static_cast<T *>(a.o)[at + e + 8 * i] = T(y);
+        for (int k = 0; k < D / 8; ++k) {
+            const float y = none ? 0.f : o[k] * inv;
+            if (a.o_fp32) static_cast<float *>(a.o)[at + e + 8 * k] = y;
+            else static_cast<T *>(a.o)[at + e + 8 * k] = T(y);
         }
         if (a.lse && e == 0)
             a.lse[head * a.nq + token] = none ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
@@ -342,7 +350,7 @@ PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices) {
 
 size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices) {
     const PagedShape s = paged_shape(c, nq, slices);
-    return (size_t)s.shares * 2 * s.rows * (c.d + 2) * sizeof(float);
+    return (size_t)s.shares * (kPagedJoinBytes + 2 * s.rows * (c.d + 2) * sizeof(float));
 }
 
 int prepare_paged(const PagedCache &c) {
@@ -413,7 +421,8 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
     a.k_end = io.k_end;
     a.o = io.o;
     a.lse = io.lse;
-    a.part = static_cast<float *>(io.workspace);
+    a.joins = static_cast<PagedJoin *>(io.workspace);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(io.workspace) + (size_t)s.shares * kPagedJoinBytes);
     a.status = c.d_status;
     a.nq = io.nq;
     a.pages = c.pages;

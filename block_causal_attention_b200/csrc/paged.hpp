@@ -12,6 +12,7 @@ namespace bca {
 
 constexpr int kPage = BCA_PAGE_TOKENS;
 constexpr int kSMs = 148;
+constexpr int kPagedJoinBytes = 32;  // of the workspace, for each share
 constexpr int kPagedTileRows = 384;  // packed rows of a work item of paged_tiles.cu
 
 // status-word bits written by the paged kernels

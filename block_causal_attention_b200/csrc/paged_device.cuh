@@ -22,10 +22,11 @@ struct PagedArgs {
     const int32_t *off, *seq, *k_begin, *k_end;  // seq null: slice i reads row i
     void *o;
     float *lse;
-    // parts of items that several blocks share: slot 2c (block c goes on with an item) and
-    // 2c + 1 (it begins one that it does not end); a slot is [rows][D] O, [rows] reference,
-    // [rows] sum, fp32
+    // Pieces of items that several blocks share: slot 2c (block c goes on with an item) and 2c + 1
+    // (it begins one that it does not end); a slot is [rows][D] O, [rows] reference, [rows] sum,
+    // fp32.  joins[c]: the item of slot 2c + 1.
     float *part;
+    struct PagedJoin *joins;
     int *status;
     int64_t nq, pages;
     int seqs, width, slices, causal;
@@ -158,11 +159,10 @@ struct PagedLocate {
     int32_t slice;
 };
 
-// The item that share c begins in (`at_end` = false), or that the cut behind it lies in.
-// All threads of the block together (a multiple of 32, at most 1024).  lo, hi: the stretch.
-// False, for the whole block, when there is none.
-__device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, bool at_end, PagedLocate &sh, uint64_t &lo,
-                                             uint64_t &hi, uint64_t &total, PagedCursor &cur) {
+// The stretch [lo, hi) of share c and the item that it begins in.  All threads of the block
+// together (a multiple of 32, at most 1024); false, for all of them, when the stretch is empty.
+__device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, PagedLocate &sh, uint64_t &lo, uint64_t &hi,
+                                             uint64_t &total, PagedCursor &cur) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
     uint64_t mine = 0, sum = 0;
     for (int i = tid; i < a.slices; i += blockDim.x) {
@@ -179,8 +179,8 @@ __device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, bool at_
     for (int w = 0; w < warps; ++w) total += sh.warp_sum[w];
     lo = paged_share(total, a.shares, c);
     hi = paged_share(total, a.shares, c + 1);
-    const uint64_t target = at_end ? hi : lo;
-    if (target >= total || (!at_end && lo == hi)) return false;
+    const uint64_t target = lo;
+    if (lo == hi) return false;
 
     uint64_t carry = 0;
     for (int base = 0; base < a.slices; base += blockDim.x) {
@@ -273,7 +273,31 @@ __device__ __forceinline__ void paged_item(const PagedArgs &a, const PagedCursor
     // token + back <= end and >= -2^31, and without the causal rule never below ke
     x.back = a.causal ? cur.s.end - (cur.s.n - 1) : INT32_MAX - cur.s.n;
     x.whole = lo <= cur.start && cur.end() <= hi;
-    x.part = 2 * c + (lo <= cur.start ? 1 : 0);
+    x.part = 2 * c + (lo <= cur.start ? 1 : 0);  // odd: begun here
+}
+
+// An item begun in share c and ended in share `last` (last < c: there is none).
+struct PagedJoin {
+    int32_t last;
+    int32_t row, token, head, left, g;  // as in PagedItem
+    int32_t unused[2];
+};
+static_assert(sizeof(PagedJoin) == kPagedJoinBytes, "workspace layout");
+
+// What the joining kernel has to know of share c, whose last item is `cur`; one thread.
+__device__ __forceinline__ void paged_join_of(const PagedArgs &a, const PagedCursor &cur, const PagedItem &x, int c,
+                                              uint64_t hi, uint64_t total) {
+    PagedJoin j = {-1, x.row, x.token, x.head, x.left, x.g, {0, 0}};
+    if (cur.end() > hi && !(x.part & 1)) j.last = -1;      // it was begun earlier
+    else if (cur.end() > hi) {
+        // the last share that begins before the item ends: an estimate, put right
+        const uint64_t end = cur.end();
+        int k = min((int)((double)end / (double)total * a.shares), a.shares - 1);
+        while (k > c && paged_share(total, a.shares, k) >= end) --k;
+        while (k + 1 < a.shares && paged_share(total, a.shares, k + 1) < end) ++k;
+        j.last = k;
+    }
+    a.joins[c] = j;
 }
 
 __device__ __forceinline__ float *paged_part(const PagedArgs &a, int d, int slot) {
@@ -394,7 +418,7 @@ __device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, const 
 // a page; an absent one holds no keys.
 template <int STAGES, int TILE, int KSTAGE, int STAGE>
 __device__ __forceinline__ void paged_fill(const PagedArgs &a, PagedCursor &cur, int c, uint64_t lo, uint64_t hi,
-                                           uint32_t ring, uint32_t bars, uint32_t item_bars, PagedItem *items,
+                                           uint64_t total, uint32_t ring, uint32_t bars, uint32_t item_bars, PagedItem *items,
                                            volatile int *here, volatile int *abort_flag) {
     const int lane = threadIdx.x & 31;
     auto full = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)i; };
@@ -442,8 +466,10 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, PagedCursor &cur,
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
         }
+        if (lane == 0 && cur.end() >= hi) paged_join_of(a, cur, x, c, hi, total);
         more = cur.end() < hi && cur.next(a);
     }
+    if (!ok && lane == 0) a.joins[c].last = -1;
     // every copy must have landed before the block may end
     if (lane == 0)
         for (int j = it > STAGES ? it - STAGES : 0; j < it; ++j)

@@ -100,11 +100,14 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     PagedCursor cur;
     uint64_t lo, hi, total;
     const int c = blockIdx.x;
-    if (!paged_locate(a, c, false, sh, lo, hi, total, cur)) return;
+    if (!paged_locate(a, c, sh, lo, hi, total, cur)) {
+        if (threadIdx.x == 0) a.joins[c].last = -1;
+        return;
+    }
     __syncthreads();
 
     if (warp == kWarps) {
-        paged_fill<S, L::TILE, L::TILE, 2 * L::TILE>(a, cur, c, lo, hi, sbase + L::OFF_RING, full(0), item_bars, items,
+        paged_fill<S, L::TILE, L::TILE, 2 * L::TILE>(a, cur, c, lo, hi, total, sbase + L::OFF_RING, full(0), item_bars, items,
                                                      here, abort_flag);
         return;
     }
@@ -314,7 +317,7 @@ ldsm_v<NV>(vs + vaddr, vf);
                     if (a.lse && e == 0)
                         a.lse[head * a.nq + token] =
                             none ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
-                } else if (p0 < p1) {
+                } else {  // without pages too: the reference, -inf, tells
                     float *part = paged_part(a, D, x.part);
 #pragma unroll
                     for (int i = 0; i < (D + 15) / 16; ++i)

@@ -97,7 +97,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
     PagedCursor cur;
     uint64_t lo, hi, total;
     const int c = blockIdx.x;
-    if (!paged_locate(a, c, false, sh, lo, hi, total, cur)) return;
+    if (!paged_locate(a, c, sh, lo, hi, total, cur)) {
+        if (threadIdx.x == 0) a.joins[c].last = -1;
+        return;
+    }
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -138,7 +141,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
     // scores among them): 128 x 56 + 384 x 152 = 65,536.
     if (warp < 4) regs_dec<56>();
     if (warp == 0) {
-        paged_fill<S, L::TILE, L::KSTAGE, L::STAGE>(a, cur, c, lo, hi, sbase + L::OFF_RING, bar(L::B_FULL),
+        paged_fill<S, L::TILE, L::KSTAGE, L::STAGE>(a, cur, c, lo, hi, total, sbase + L::OFF_RING, bar(L::B_FULL),
                                                     bar(L::B_ITEM), items, here, abort_flag);
     } else if (warp == 1) {
         // ------------------------------------------------ S = Q K^T
@@ -531,7 +534,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                         }
                         if (a.lse && t == 0)
                             a.lse[head * a.nq + token] = none ? -INFINITY : (ref[m][h] + log2f(l)) * 0.69314718055994531f;
-                    } else if (p0 < p1) {
+                    } else {  // without pages too: the reference, -inf, tells
 #pragma unroll
                         for (int n = 0; n < NV; ++n)
                             *reinterpret_cast<float2 *>(part + (size_t)r * D + 8 * n + 2 * t) =
