@@ -4,6 +4,7 @@
 #include <cuda_runtime.h>
 
 #include <algorithm>
+#include <cmath>
 #include <cstring>
 #include <type_traits>
 
@@ -264,7 +265,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
             if (top == -INFINITY) continue;
             const float keep = ref == -INFINITY ? 0.f : sm100::ex2(ref - top);
             const float w = r == -INFINITY ? 0.f : sm100::ex2(r - top);
-            l *= w;
+            l = r == -INFINITY ? 0.f : l * w;  // (a piece without keys may have no sum)
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
             sum = sum * keep + l;
@@ -441,9 +442,12 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
     a.timeout_ns = (c.flags & BCA_TEST_FORCE_TIMEOUT) ? 1000000ull : kPagedWaitNs;
     a.skip_loads = (c.flags & BCA_TEST_FORCE_TIMEOUT) ? 1 : 0;
     std::memcpy(a.turns, c.turns, sizeof(a.turns));
-    // the row of items must stay below 2^62 long (rows of q and tables this large do not fit a GPU)
-    const double tiles = (double)io.nq * a.group / a.rows + io.slices;
-    if (tiles * c.hkv * ((double)io.width * kPage + (double)io.nq + kItemWeight) > 4e18) return BCA_ERR_TOO_LARGE;
+    // The row of items, at its longest: see paged_device.cuh.
+    const double items = ((double)io.nq * a.group / a.rows + io.slices) * c.hkv;
+    const double keys = std::max((double)io.width * kPage, (double)io.nq);
+    a.shift = 0;
+    while (a.shift < 27 && items * (16.0 + std::ldexp(keys, -4 - a.shift)) > 2e9) ++a.shift;
+    if (items * 17.0 > 2e9) return BCA_ERR_TOO_LARGE;
     const int rc = a.rows == kPagedTileRows ? launch_paged_tiles(c, a, stream) : launch_paged_rows(c, a, stream);
     if (rc != BCA_OK) return rc;
     return by_type(c, [&](auto d, auto t) { return launch_join<decltype(d)::value, decltype(t)>(a, stream); });

@@ -33,6 +33,7 @@ struct PagedArgs {
     int hq, hkv, group;
     int rows;             // packed rows of a tile
     int shares;           // blocks of the attention kernel
+    int shift;            // a unit of weight is 16 << shift keys
     int o_fp32;
     float eps;
     float scale;          // log2(e) / sqrt(D)
@@ -52,22 +53,24 @@ struct PagedArgs {
 // lengths are (they are device data), and the cut depends on the arguments alone: the same
 // call gives the same bits.
 
-// Weight of an item that reads no page, in keys: its prologue, its epilogue and the start
-// of its loads.
-constexpr int64_t kItemWeight = 128;
+// Weight of an item that reads no page, in units of 16 << shift keys: its prologue, its epilogue
+// and the start of its loads, worth a page.  The whole row of items is below 2^31 units long
+// (the host picks the shift for the sizes of the call), so all of this is 32-bit arithmetic:
+// before a block knows what to load it can do nothing else, and 64-bit divisions here took 2 us.
+constexpr uint32_t kItemWeight = 8;
 
 struct PagedSlice {
     int32_t r0, n;        // its rows of q
     int32_t b;            // table row
     int32_t kb, ke;       // keys [kb, ke) that it sees; kb == ke: none
     int32_t end;          // k_end as given (>= 0): the causal rule counts back from it
-    int64_t tiles;        // of one KV head
-    int64_t w0, dw;       // weight of tile t: w0 + dw * (t + 1)
+    uint32_t tiles;       // of one KV head
+    uint32_t w0, dw;      // weight of tile t: w0 + dw * (t + 1)
 
-    __device__ __forceinline__ uint64_t upto(int64_t t) const {  // weight of its first t tiles
-        return (uint64_t)(t * w0 + dw * (t * (t + 1) / 2));
+    __device__ __forceinline__ uint32_t upto(uint32_t t) const {  // weight of its first t tiles
+        return t * w0 + (dw == 0 ? 0u : dw * (t * (t + 1) / 2));
     }
-    __device__ __forceinline__ uint64_t weight(int64_t t) const { return (uint64_t)(w0 + dw * (t + 1)); }
+    __device__ __forceinline__ uint32_t weight(uint32_t t) const { return w0 + dw * (t + 1); }
 };
 
 __device__ __forceinline__ PagedSlice paged_slice(const PagedArgs &a, int i) {
@@ -82,14 +85,16 @@ __device__ __forceinline__ PagedSlice paged_slice(const PagedArgs &a, int i) {
     s.kb = max(kb, 0);
     s.ke = min(s.end, a.width * kPage);
     if (b < 0 || b >= a.seqs || s.ke <= s.kb) s.kb = s.ke = 0;
-    s.tiles = ((int64_t)s.n * a.group + a.rows - 1) / a.rows;
-    const int64_t keys = s.ke - s.kb;
+    // n * group rows: below 2^32, since Q itself fits a GPU
+    s.tiles = (uint32_t)(((uint64_t)(uint32_t)s.n * (uint32_t)a.group + (uint32_t)(a.rows - 1)) / (uint32_t)a.rows);
+    const int32_t keys = s.ke - s.kb;
+    const int unit = 4 + a.shift;
     if (a.causal) {
-        s.dw = a.rows / a.group;
-        s.w0 = kItemWeight + max(keys - s.n, (int64_t)0);
+        s.dw = (uint32_t)(a.rows / a.group) >> unit;
+        s.w0 = kItemWeight + ((uint32_t)max(keys - s.n, 0) >> unit);
     } else {
         s.dw = 0;
-        s.w0 = kItemWeight + keys;
+        s.w0 = kItemWeight + ((uint32_t)keys >> unit);
     }
     return s;
 }
@@ -100,30 +105,36 @@ __device__ __forceinline__ int32_t paged_limit(const PagedArgs &a, const PagedSl
     return min(s.ke, s.end - (s.n - 1 - token));  // no overflow: both are >= 0 and below 2^31
 }
 
-// Where share c begins in a row of this total weight.
-__device__ __forceinline__ uint64_t paged_share(uint64_t total, int shares, int c) {
-    return total / shares * c + total % shares * c / shares;
+// Where share c begins in a row of this total weight: total * c / shares.
+__device__ __forceinline__ uint32_t paged_share(uint32_t total, int shares, int c) {
+    const uint32_t n = (uint32_t)shares, x = (uint32_t)c;
+    return total / n * x + total % n * x / n;
 }
 
 struct PagedCursor {
     PagedSlice s;
     int32_t slice;
     int32_t g;          // KV head
-    int64_t t;          // tile
-    uint64_t start;     // where the item begins
+    uint32_t t;         // tile
+    uint32_t start;     // where the item begins
 
-    __device__ __forceinline__ uint64_t end() const { return start + s.weight(t); }
+    __device__ __forceinline__ uint32_t end() const { return start + s.weight(t); }
 
-    // Pages of the item, and the part of them that lies in [lo, hi).
-    __device__ __forceinline__ void pages(const PagedArgs &a, uint64_t lo, uint64_t hi, int32_t &p0,
+    // Pages of the item, and the part of them that lies in [lo, hi).  A cut inside the item takes
+    // its share of the pages in fp32: any rounding does, as long as it never falls along the item
+    // and is the same in the two blocks that meet there.
+    __device__ __forceinline__ void pages(const PagedArgs &a, uint32_t lo, uint32_t hi, int32_t &p0,
                                           int32_t &p1) const {
-        const int64_t last = min(((t + 1) * a.rows - 1) / a.group, (int64_t)s.n - 1);
-        const int32_t ke = paged_limit(a, s, (int32_t)last);
+        const uint64_t after = (uint64_t)(t + 1) * (uint32_t)a.rows - 1;
+        const int32_t last = (int32_t)min((uint32_t)(after / (uint32_t)a.group), (uint32_t)(s.n - 1));
+        const int32_t ke = paged_limit(a, s, last);
         const int32_t first = s.kb / kPage;
-        const uint64_t np = ke > s.kb ? (uint64_t)((ke - 1) / kPage + 1 - first) : 0;
-        const uint64_t w = s.weight(t);
-        p0 = first + (lo > start ? (int32_t)(np * (lo - start) / w) : 0);
-        p1 = first + (int32_t)(hi < start + w ? np * (hi - start) / w : np);
+        const int32_t np = ke > s.kb ? (ke - 1) / kPage + 1 - first : 0;
+        const uint32_t w = s.weight(t);
+        const float ratio = __fdiv_rn((float)np, (float)w);
+        p0 = first + (lo > start ? min(np, (int32_t)__fmul_rn((float)(lo - start), ratio)) : 0);
+        p1 = first + (hi < start + w ? min(np, (int32_t)__fmul_rn((float)(hi - start), ratio)) : np);
+        p1 = max(p0, p1);
     }
 
     // The next item (all 32 lanes of a warp together: slices without rows are passed over 32
@@ -153,88 +164,83 @@ struct PagedCursor {
     }
 };
 
-struct PagedLocate {
-    uint64_t warp_sum[32];
-    uint64_t pre;
-    int32_t slice;
-};
-
-// The stretch [lo, hi) of share c and the item that it begins in.  All threads of the block
-// together (a multiple of 32, at most 1024); false, for all of them, when the stretch is empty.
-__device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, PagedLocate &sh, uint64_t &lo, uint64_t &hi,
-                                             uint64_t &total, PagedCursor &cur) {
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = blockDim.x >> 5;
-    uint64_t mine = 0, sum = 0;
-    for (int i = tid; i < a.slices; i += blockDim.x) {
-        const PagedSlice s = paged_slice(a, i);
-        mine = a.hkv * s.upto(s.tiles);
-        sum += mine;
-    }
+// The stretch [lo, hi) of share c and the item that it begins in, found by one warp: four
+// slices a lane at a time.  False when the stretch is empty.
+__device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, uint32_t &lo, uint32_t &hi, uint32_t &total,
+                                             PagedCursor &cur) {
+    constexpr int U = 4;
+    const int lane = threadIdx.x & 31;
+    uint32_t mine[U], sum = 0;
+    auto load = [&](int base) {
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) sh.warp_sum[warp] = sum;
-    if (tid == 0) sh.slice = -1;
-    __syncthreads();
-    total = 0;
-    for (int w = 0; w < warps; ++w) total += sh.warp_sum[w];
-    lo = paged_share(total, a.shares, c);
-    hi = paged_share(total, a.shares, c + 1);
-    const uint64_t target = lo;
-    if (lo == hi) return false;
-
-    uint64_t carry = 0;
-    for (int base = 0; base < a.slices; base += blockDim.x) {
-        const int i = base + tid;
-        if (a.slices > (int)blockDim.x) {
-            mine = 0;
+        for (int u = 0; u < U; ++u) {
+            const int i = base + U * lane + u;
+            mine[u] = 0;
             if (i < a.slices) {
                 const PagedSlice s = paged_slice(a, i);
-                mine = a.hkv * s.upto(s.tiles);
+                mine[u] = (uint32_t)a.hkv * s.upto(s.tiles);
             }
         }
-        uint64_t inc = mine;
+    };
+    for (int base = 0; base < a.slices; base += 32 * U) {
+        load(base);
+#pragma unroll
+        for (int u = 0; u < U; ++u) sum += mine[u];
+    }
+    total = __reduce_add_sync(0xffffffffu, sum);
+    lo = paged_share(total, a.shares, c);
+    hi = paged_share(total, a.shares, c + 1);
+    if (lo == hi) return false;
+
+    // (offsets that do not rise may make the whole longer than 2^32, and then nothing be found)
+    uint32_t carry = 0, at = 0;
+    cur.slice = -1;
+    for (int base = 0; base < a.slices; base += 32 * U) {
+        if (a.slices > 32 * U) load(base);
+        uint32_t here = 0;
+#pragma unroll
+        for (int u = 0; u < U; ++u) here += mine[u];
+        uint32_t inc = here;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
-            const uint64_t v = __shfl_up_sync(0xffffffffu, inc, o);
+            const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
-        __syncthreads();
-        if (lane == 31) sh.warp_sum[warp] = inc;
-        __syncthreads();
-        uint64_t before = carry, block = 0;
-        for (int w = 0; w < warps; ++w) {
-            if (w < warp) before += sh.warp_sum[w];
-            block += sh.warp_sum[w];
-        }
-        const uint64_t pre = before + inc - mine;
-        if (pre <= target && target - pre < mine) {
-            sh.slice = i;
-            sh.pre = pre;
+        const uint32_t block = __shfl_sync(0xffffffffu, inc, 31);
+        if (lo - carry < block) {
+            uint32_t pre = carry + inc - here;
+            const int src = __ffs(__ballot_sync(0xffffffffu, lo - pre < here && pre <= lo)) - 1;
+            if (src < 0) break;
+            int u = 0;
+#pragma unroll
+            for (int k = 0; k + 1 < U; ++k)
+                if (u == k && lo - pre >= mine[k]) {
+                    pre += mine[k];
+                    u = k + 1;
+                }
+            cur.slice = base + U * src + __shfl_sync(0xffffffffu, u, src);
+            at = __shfl_sync(0xffffffffu, pre, src);
+            break;
         }
         carry += block;
-        if (carry > target) break;
     }
-    __syncthreads();
-    cur.slice = sh.slice;
     if (cur.slice < 0) return false;
     cur.s = paged_slice(a, cur.slice);
-    const uint64_t per_head = cur.s.upto(cur.s.tiles);
-    uint64_t rest = target - sh.pre;
+    const uint32_t per_head = cur.s.upto(cur.s.tiles);
+    uint32_t rest = lo - at;
     cur.g = (int32_t)(rest / per_head);
-    rest %= per_head;
-    int64_t t;
-    if (cur.s.dw == 0) {
-        t = (int64_t)(rest / (uint64_t)cur.s.w0);
-    } else {
+    rest -= (uint32_t)cur.g * per_head;
+    uint32_t t = rest / cur.s.w0;
+    if (cur.s.dw != 0) {
         // upto(t) <= rest, a quadratic in t; the loops take the rounding out
-        const double h = (double)cur.s.w0 + 0.5 * cur.s.dw;
-        t = (int64_t)((sqrt(h * h + 2.0 * cur.s.dw * (double)rest) - h) / cur.s.dw);
+        const float h = (float)cur.s.w0 + 0.5f * cur.s.dw;
+        t = (uint32_t)((sqrtf(h * h + 2.0f * cur.s.dw * (float)rest) - h) / cur.s.dw);
     }
-    t = min(max(t, (int64_t)0), cur.s.tiles - 1);
+    t = min(t, cur.s.tiles - 1);
     while (t > 0 && cur.s.upto(t) > rest) --t;
     while (t + 1 < cur.s.tiles && cur.s.upto(t + 1) <= rest) ++t;
     cur.t = t;
-    cur.start = target - (rest - cur.s.upto(t));
+    cur.start = lo - (rest - cur.s.upto(t));
     return true;
 }
 
@@ -259,14 +265,14 @@ struct PagedItem {
     }
 };
 
-__device__ __forceinline__ void paged_item(const PagedArgs &a, const PagedCursor &cur, int c, uint64_t lo,
-                                           uint64_t hi, PagedItem &x) {
+__device__ __forceinline__ void paged_item(const PagedArgs &a, const PagedCursor &cur, int c, uint32_t lo,
+                                           uint32_t hi, PagedItem &x) {
     cur.pages(a, lo, hi, x.p0, x.p1);
-    const int64_t first = cur.t * a.rows;
+    const uint64_t first = (uint64_t)cur.t * (uint32_t)a.rows;
     x.row = cur.s.r0;
-    x.token = (int32_t)(first / a.group);
-    x.head = (int32_t)(first % a.group);
-    x.left = (int32_t)min((int64_t)cur.s.n * a.group - first, (int64_t)a.rows);
+    x.token = (int32_t)(first / (uint32_t)a.group);
+    x.head = (int32_t)(first - (uint64_t)x.token * (uint32_t)a.group);
+    x.left = (int32_t)min((uint64_t)(uint32_t)cur.s.n * (uint32_t)a.group - first, (uint64_t)a.rows);
     x.g = cur.g;
     x.kb = cur.s.kb;
     x.ke = cur.s.ke;
@@ -286,13 +292,13 @@ static_assert(sizeof(PagedJoin) == kPagedJoinBytes, "workspace layout");
 
 // What the joining kernel has to know of share c, whose last item is `cur`; one thread.
 __device__ __forceinline__ void paged_join_of(const PagedArgs &a, const PagedCursor &cur, const PagedItem &x, int c,
-                                              uint64_t hi, uint64_t total) {
+                                              uint32_t hi, uint32_t total) {
     PagedJoin j = {-1, x.row, x.token, x.head, x.left, x.g, {0, 0}};
     if (cur.end() > hi && !(x.part & 1)) j.last = -1;      // it was begun earlier
     else if (cur.end() > hi) {
         // the last share that begins before the item ends: an estimate, put right
-        const uint64_t end = cur.end();
-        int k = min((int)((double)end / (double)total * a.shares), a.shares - 1);
+        const uint32_t end = cur.end();
+        int k = min((int)((float)end / (float)total * a.shares), a.shares - 1);
         while (k > c && paged_share(total, a.shares, k) >= end) --k;
         while (k + 1 < a.shares && paged_share(total, a.shares, k + 1) < end) ++k;
         j.last = k;
@@ -360,17 +366,23 @@ struct Row8 {
     static constexpr int N = (D / 2 + 7) / 8;
     float2 x[N];
 
+    float2 gn[N];
+    int32_t at[N];
+
+    // Everything that the row needs from memory, on the way at the same time.
     template <typename T>
-    __device__ __forceinline__ void load(const T *row, int e) {
+    __device__ __forceinline__ void load(const T *row, const int32_t *pos, const float *gain, int e) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int p = e + 8 * i;
             x[i] = p < D / 2 ? Io<T>::unpack(__ldg(reinterpret_cast<const uint32_t *>(row) + p)) : float2{0.f, 0.f};
+            at[i] = pos && p < 3 * P ? __ldg(pos + p / P) : 0;
+            gn[i] = pos && gain && p < D / 2 ? make_float2(__ldg(gain + 2 * p), __ldg(gain + 2 * p + 1))
+                                             : make_float2(1.f, 1.f);
         }
     }
 
-    __device__ __forceinline__ void prologue(const int32_t *pos, const float *gain, const double *turns, float eps,
-                                             int e) {
+    __device__ __forceinline__ void prologue(const double *turns, float eps, int e) {
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) ss = fmaf(x[i].x, x[i].x, fmaf(x[i].y, x[i].y, ss));
@@ -380,18 +392,11 @@ struct Row8 {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int p = e + 8 * i;
-            if (p >= D / 2) continue;
-            float y0 = x[i].x * r, y1 = x[i].y * r;
-            if (gain) {
-                y0 *= __ldg(gain + 2 * p);
-                y1 *= __ldg(gain + 2 * p + 1);
-            }
+            const float y0 = x[i].x * r * gn[i].x, y1 = x[i].y * r * gn[i].y;
+            x[i] = make_float2(y0, y1);
             if (p < 3 * P) {
-                const int axis = p / P;
-                const float2 cs = paged_cos_sin(__ldg(pos + axis), turns[8 * axis + p - axis * P]);
+                const float2 cs = paged_cos_sin(at[i], turns[8 * (p / P) + p % P]);
                 x[i] = make_float2(y0 * cs.x - y1 * cs.y, y0 * cs.y + y1 * cs.x);
-            } else {
-                x[i] = make_float2(y0, y1);
             }
         }
     }
@@ -411,20 +416,26 @@ __device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, const 
     return false;
 }
 
-// The warp that walks the items: publishes each and moves its pages into the ring, a page's
+// The warp that walks the items of share c: publishes each and moves its pages into the ring, a page's
 // keys and values by one bulk copy each, until the block's stretch ends; then waits for the
 // copies that are still in flight.  Barriers: full / empty of the STAGES page stages (base +
 // 8 i, base + 8 (STAGES + i)), and of the kItemRing items behind them.  here[i]: stage i holds
 // a page; an absent one holds no keys.
 template <int STAGES, int TILE, int KSTAGE, int STAGE>
-__device__ __forceinline__ void paged_fill(const PagedArgs &a, PagedCursor &cur, int c, uint64_t lo, uint64_t hi,
-                                           uint64_t total, uint32_t ring, uint32_t bars, uint32_t item_bars, PagedItem *items,
+__device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t ring, uint32_t bars, uint32_t item_bars, PagedItem *items,
                                            volatile int *here, volatile int *abort_flag) {
     const int lane = threadIdx.x & 31;
     auto full = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)i; };
     auto empty = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)(STAGES + i); };
+    PagedCursor cur;
+    uint32_t lo, hi, total;
     int it = 0;
-    bool ok = true, more = true;
+    bool ok = true, more = paged_locate(a, c, lo, hi, total, cur);
+    if (!more) {
+        // an empty stretch inside an item that others share: a piece without keys
+        if (lane == 0) a.joins[c].last = -1;
+        for (int r = lane; r < a.rows; r += 32) paged_part(a, TILE / (2 * kPage), 2 * c)[a.rows * (TILE / (2 * kPage)) + r] = -INFINITY;
+    }
     for (int n = 0; ok; ++n) {
         const int slot = n % kItemRing;
         if (n >= kItemRing)

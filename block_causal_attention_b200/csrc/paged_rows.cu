@@ -73,7 +73,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     constexpr float kShift = Io<T>::kShift;
 
     extern __shared__ __align__(128) uint8_t smem[];
-    __shared__ PagedLocate sh;
     const uint32_t sbase = smem_u32(smem);
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
     volatile int *here = reinterpret_cast<volatile int *>(smem + L::OFF_HERE);
@@ -97,17 +96,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         }
         mbar_fence_init();
     }
-    PagedCursor cur;
-    uint64_t lo, hi, total;
     const int c = blockIdx.x;
-    if (!paged_locate(a, c, sh, lo, hi, total, cur)) {
-        if (threadIdx.x == 0) a.joins[c].last = -1;
-        return;
-    }
     __syncthreads();
 
     if (warp == kWarps) {
-        paged_fill<S, L::TILE, L::TILE, 2 * L::TILE>(a, cur, c, lo, hi, total, sbase + L::OFF_RING, full(0), item_bars, items,
+        paged_fill<S, L::TILE, L::TILE, 2 * L::TILE>(a, c, sbase + L::OFF_RING, full(0), item_bars, items,
                                                      here, abort_flag);
         return;
     }
@@ -140,8 +133,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
             const uint32_t packed = x.head + (live ? r : 0);
             const int64_t row = x.row + x.token + (int32_t)(packed / a.group);
             Row8<D> q;
-            q.load(static_cast<const T *>(a.q) + (row * a.hq + x.g * a.group + packed % a.group) * D, e);
-            if (a.pos) q.prologue(a.pos + row * 3, a.q_gain, a.turns, a.eps, e);
+            q.load(static_cast<const T *>(a.q) + (row * a.hq + x.g * a.group + packed % a.group) * D,
+                   a.pos ? a.pos + row * 3 : nullptr, a.q_gain, e);
+            if (a.pos) q.prologue(a.turns, a.eps, e);
 #pragma unroll
             for (int i = 0; i < Row8<D>::N; ++i)
                 if (e + 8 * i < D / 2)

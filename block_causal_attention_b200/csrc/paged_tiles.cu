@@ -84,7 +84,6 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
     constexpr float kShift = Io<T>::kShift;
 
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ PagedLocate sh;
     const uint32_t sbase = smem_u32(smem);
     auto bar = [&](int i) -> uint32_t { return sbase + L::OFF_BAR + 8u * (uint32_t)i; };
     volatile int *abort_flag = reinterpret_cast<volatile int *>(smem + L::OFF_ABORT);
@@ -94,13 +93,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    PagedCursor cur;
-    uint64_t lo, hi, total;
     const int c = blockIdx.x;
-    if (!paged_locate(a, c, sh, lo, hi, total, cur)) {
-        if (threadIdx.x == 0) a.joins[c].last = -1;
-        return;
-    }
 
     if (threadIdx.x == 0) {
         *abort_flag = 0;
@@ -141,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
     // scores among them): 128 x 56 + 384 x 152 = 65,536.
     if (warp < 4) regs_dec<56>();
     if (warp == 0) {
-        paged_fill<S, L::TILE, L::KSTAGE, L::STAGE>(a, cur, c, lo, hi, total, sbase + L::OFF_RING, bar(L::B_FULL),
+        paged_fill<S, L::TILE, L::KSTAGE, L::STAGE>(a, c, sbase + L::OFF_RING, bar(L::B_FULL),
                                                     bar(L::B_ITEM), items, here, abort_flag);
     } else if (warp == 1) {
         // ------------------------------------------------ S = Q K^T
@@ -249,8 +242,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                     const uint32_t packed = x.head + (live ? slot * 128 + r : 0);
                     const int64_t row = x.row + x.token + (int32_t)(packed / a.group);
                     Row8<D> q;
-                    q.load(static_cast<const T *>(a.q) + (row * a.hq + x.g * a.group + packed % a.group) * D, e);
-                    if (a.pos) q.prologue(a.pos + row * 3, a.q_gain, a.turns, a.eps, e);
+                    q.load(static_cast<const T *>(a.q) + (row * a.hq + x.g * a.group + packed % a.group) * D,
+                   a.pos ? a.pos + row * 3 : nullptr, a.q_gain, e);
+                    if (a.pos) q.prologue(a.turns, a.eps, e);
 #pragma unroll
                     for (int k = 0; k < Row8<D>::N; ++k) {
                         const int pr = e + 8 * k;
