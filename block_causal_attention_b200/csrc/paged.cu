@@ -40,7 +40,7 @@ struct WriteArgs {
     int64_t n, pages;
     int seqs, width, hkv;
     float eps;
-    double turns[24];
+    uint64_t turns[24];
 };
 
 // The block of 32-aligned tokens that this grid block has.  Sequence b begins at grid block

@@ -24,8 +24,9 @@ struct PagedCache {
     int64_t pages = 0;
     float eps = 1e-6f;
     uint32_t flags = 0;
-    // turns per unit of position of pair i of axis a: base_a^(-i/P) / 2 pi, at [8 a + i]
-    double turns[24] = {};
+    // turns per unit of position of pair i of axis a: base_a^(-i/P) / 2 pi without the whole
+    // ones, in units of 2^-64, at [8 a + i]
+    uint64_t turns[24] = {};
     int device = -1;
     int *d_status = nullptr;
 };

@@ -44,8 +44,11 @@ int fill(const bca_paged_desc *d, PagedCache &c) {
     c.flags = d->flags;
     const int pairs = c.d / 2 / 3;
     for (int a = 0; a < 3; ++a)
-        for (int i = 0; i < pairs; ++i)
-            c.turns[8 * a + i] = std::pow((double)d->rope_base[a], -(double)i / pairs) / 6.283185307179586476925;
+        for (int i = 0; i < pairs; ++i) {
+            const long double x = std::pow((long double)d->rope_base[a], -(long double)i / pairs) /
+                                  6.283185307179586476925286766559L;
+            c.turns[8 * a + i] = (uint64_t)std::ldexp(x - std::floor(x), 64);  // below 2^64
+        }
     return BCA_OK;
 }
 

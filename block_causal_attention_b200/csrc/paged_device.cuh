@@ -39,7 +39,7 @@ struct PagedArgs {
     float scale;          // log2(e) / sqrt(D)
     uint64_t timeout_ns;
     int skip_loads;       // failure-detection test: issue no page loads
-    double turns[24];
+    uint64_t turns[24];
 };
 
 // ------------------------------------------------------------------ the work and its shares
@@ -73,6 +73,7 @@ struct PagedSlice {
     __device__ __forceinline__ uint32_t weight(uint32_t t) const { return w0 + dw * (t + 1); }
 };
 
+template <int R>
 __device__ __forceinline__ PagedSlice paged_slice(const PagedArgs &a, int i) {
     PagedSlice s;
     const int32_t nq = (int32_t)a.nq;
@@ -86,11 +87,11 @@ __device__ __forceinline__ PagedSlice paged_slice(const PagedArgs &a, int i) {
     s.ke = min(s.end, a.width * kPage);
     if (b < 0 || b >= a.seqs || s.ke <= s.kb) s.kb = s.ke = 0;
     // n * group rows: below 2^32, since Q itself fits a GPU
-    s.tiles = (uint32_t)(((uint64_t)(uint32_t)s.n * (uint32_t)a.group + (uint32_t)(a.rows - 1)) / (uint32_t)a.rows);
+    s.tiles = ((uint32_t)s.n * (uint32_t)a.group + (R - 1)) / R;
     const int32_t keys = s.ke - s.kb;
     const int unit = 4 + a.shift;
     if (a.causal) {
-        s.dw = (uint32_t)(a.rows / a.group) >> unit;
+        s.dw = (uint32_t)R / (uint32_t)a.group >> unit;
         s.w0 = kItemWeight + ((uint32_t)max(keys - s.n, 0) >> unit);
     } else {
         s.dw = 0;
@@ -111,6 +112,7 @@ __device__ __forceinline__ uint32_t paged_share(uint32_t total, int shares, int 
     return total / n * x + total % n * x / n;
 }
 
+template <int R>
 struct PagedCursor {
     PagedSlice s;
     int32_t slice;
@@ -125,9 +127,8 @@ struct PagedCursor {
     // and is the same in the two blocks that meet there.
     __device__ __forceinline__ void pages(const PagedArgs &a, uint32_t lo, uint32_t hi, int32_t &p0,
                                           int32_t &p1) const {
-        const uint64_t after = (uint64_t)(t + 1) * (uint32_t)a.rows - 1;
-        const int32_t last = (int32_t)min((uint32_t)(after / (uint32_t)a.group), (uint32_t)(s.n - 1));
-        const int32_t ke = paged_limit(a, s, last);
+        const uint32_t last = min(((t + 1) * R - 1) / (uint32_t)a.group, (uint32_t)(s.n - 1));
+        const int32_t ke = a.causal ? paged_limit(a, s, (int32_t)last) : s.ke;
         const int32_t first = s.kb / kPage;
         const int32_t np = ke > s.kb ? (ke - 1) / kPage + 1 - first : 0;
         const uint32_t w = s.weight(t);
@@ -156,7 +157,7 @@ struct PagedCursor {
             const uint32_t m = __ballot_sync(0xffffffffu, some);
             if (m) {
                 slice = base + __ffs(m) - 1;
-                s = paged_slice(a, slice);
+                s = paged_slice<R>(a, slice);
                 return true;
             }
         }
@@ -164,28 +165,19 @@ struct PagedCursor {
     }
 };
 
-// The stretch [lo, hi) of share c and the item that it begins in, found by one warp: four
-// slices a lane at a time.  False when the stretch is empty.
+// The stretch [lo, hi) of share c and the item that it begins in, found by one warp, a slice a
+// lane at a time.  False when the stretch is empty.
+template <int R>
 __device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, uint32_t &lo, uint32_t &hi, uint32_t &total,
-                                             PagedCursor &cur) {
-    constexpr int U = 4;
+                                             PagedCursor<R> &cur) {
     const int lane = threadIdx.x & 31;
-    uint32_t mine[U], sum = 0;
-    auto load = [&](int base) {
-#pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const int i = base + U * lane + u;
-            mine[u] = 0;
-            if (i < a.slices) {
-                const PagedSlice s = paged_slice(a, i);
-                mine[u] = (uint32_t)a.hkv * s.upto(s.tiles);
-            }
-        }
-    };
-    for (int base = 0; base < a.slices; base += 32 * U) {
-        load(base);
-#pragma unroll
-        for (int u = 0; u < U; ++u) sum += mine[u];
+    PagedSlice s;
+    uint32_t mine = 0, sum = 0;
+#pragma unroll 1
+    for (int i = lane; i < a.slices; i += 32) {
+        s = paged_slice<R>(a, i);
+        mine = (uint32_t)a.hkv * s.upto(s.tiles);
+        sum += mine;
     }
     total = __reduce_add_sync(0xffffffffu, sum);
     lo = paged_share(total, a.shares, c);
@@ -193,52 +185,55 @@ __device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, uint32_t
     if (lo == hi) return false;
 
     // (offsets that do not rise may make the whole longer than 2^32, and then nothing be found)
-    uint32_t carry = 0, at = 0;
-    cur.slice = -1;
-    for (int base = 0; base < a.slices; base += 32 * U) {
-        if (a.slices > 32 * U) load(base);
-        uint32_t here = 0;
-#pragma unroll
-        for (int u = 0; u < U; ++u) here += mine[u];
-        uint32_t inc = here;
+    uint32_t carry = 0, pre = 0;
+    int src = -1;
+#pragma unroll 1
+    for (int base = 0; base < a.slices && src < 0; base += 32) {
+        if (a.slices > 32) {
+            mine = 0;
+            if (base + lane < a.slices) {
+                s = paged_slice<R>(a, base + lane);
+                mine = (uint32_t)a.hkv * s.upto(s.tiles);
+            }
+        }
+        uint32_t inc = mine;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
             const uint32_t v = __shfl_up_sync(0xffffffffu, inc, o);
             if (lane >= o) inc += v;
         }
-        const uint32_t block = __shfl_sync(0xffffffffu, inc, 31);
-        if (lo - carry < block) {
-            uint32_t pre = carry + inc - here;
-            const int src = __ffs(__ballot_sync(0xffffffffu, lo - pre < here && pre <= lo)) - 1;
-            if (src < 0) break;
-            int u = 0;
-#pragma unroll
-            for (int k = 0; k + 1 < U; ++k)
-                if (u == k && lo - pre >= mine[k]) {
-                    pre += mine[k];
-                    u = k + 1;
-                }
-            cur.slice = base + U * src + __shfl_sync(0xffffffffu, u, src);
-            at = __shfl_sync(0xffffffffu, pre, src);
-            break;
-        }
-        carry += block;
+        pre = carry + inc - mine;
+        src = __ffs(__ballot_sync(0xffffffffu, pre <= lo && lo - pre < mine)) - 1;
+        carry += __shfl_sync(0xffffffffu, inc, 31);
+        cur.slice = base + src;
     }
-    if (cur.slice < 0) return false;
-    cur.s = paged_slice(a, cur.slice);
+    if (src < 0) return false;
+    auto give = [&](auto x) { return __shfl_sync(0xffffffffu, x, src); };
+    cur.s.r0 = give(s.r0);
+    cur.s.n = give(s.n);
+    cur.s.b = give(s.b);
+    cur.s.kb = give(s.kb);
+    cur.s.ke = give(s.ke);
+    cur.s.end = give(s.end);
+    cur.s.tiles = give(s.tiles);
+    cur.s.w0 = give(s.w0);
+    cur.s.dw = give(s.dw);
     const uint32_t per_head = cur.s.upto(cur.s.tiles);
-    uint32_t rest = lo - at;
+    uint32_t rest = lo - give(pre);
     cur.g = (int32_t)(rest / per_head);
     rest -= (uint32_t)cur.g * per_head;
-    uint32_t t = rest / cur.s.w0;
-    if (cur.s.dw != 0) {
-        // upto(t) <= rest, a quadratic in t; the loops take the rounding out
-        const float h = (float)cur.s.w0 + 0.5f * cur.s.dw;
-        t = (uint32_t)((sqrtf(h * h + 2.0f * cur.s.dw * (float)rest) - h) / cur.s.dw);
+    uint32_t t = 0;
+    if (cur.s.tiles > 1) {
+        t = rest / cur.s.w0;
+        if (cur.s.dw != 0) {
+            // upto(t) <= rest, a quadratic in t; the loops take the rounding out
+            const float h = (float)cur.s.w0 + 0.5f * cur.s.dw;
+            t = (uint32_t)((sqrtf(h * h + 2.0f * cur.s.dw * (float)rest) - h) / cur.s.dw);
+        }
+        t = min(t, cur.s.tiles - 1);
+        while (t > 0 && cur.s.upto(t) > rest) --t;
+        while (t + 1 < cur.s.tiles && cur.s.upto(t + 1) <= rest) ++t;
     }
-    t = min(t, cur.s.tiles - 1);
-    while (t > 0 && cur.s.upto(t) > rest) --t;
-    while (t + 1 < cur.s.tiles && cur.s.upto(t + 1) <= rest) ++t;
     cur.t = t;
     cur.start = lo - (rest - cur.s.upto(t));
     return true;
@@ -265,14 +260,15 @@ struct PagedItem {
     }
 };
 
-__device__ __forceinline__ void paged_item(const PagedArgs &a, const PagedCursor &cur, int c, uint32_t lo,
+template <int R>
+__device__ __forceinline__ void paged_item(const PagedArgs &a, const PagedCursor<R> &cur, int c, uint32_t lo,
                                            uint32_t hi, PagedItem &x) {
     cur.pages(a, lo, hi, x.p0, x.p1);
-    const uint64_t first = (uint64_t)cur.t * (uint32_t)a.rows;
+    const uint32_t first = cur.t * R;
     x.row = cur.s.r0;
     x.token = (int32_t)(first / (uint32_t)a.group);
-    x.head = (int32_t)(first - (uint64_t)x.token * (uint32_t)a.group);
-    x.left = (int32_t)min((uint64_t)(uint32_t)cur.s.n * (uint32_t)a.group - first, (uint64_t)a.rows);
+    x.head = (int32_t)(first - (uint32_t)x.token * (uint32_t)a.group);
+    x.left = (int32_t)min((uint32_t)cur.s.n * (uint32_t)a.group - first, (uint32_t)R);
     x.g = cur.g;
     x.kb = cur.s.kb;
     x.ke = cur.s.ke;
@@ -291,7 +287,8 @@ struct PagedJoin {
 static_assert(sizeof(PagedJoin) == kPagedJoinBytes, "workspace layout");
 
 // What the joining kernel has to know of share c, whose last item is `cur`; one thread.
-__device__ __forceinline__ void paged_join_of(const PagedArgs &a, const PagedCursor &cur, const PagedItem &x, int c,
+template <int R>
+__device__ __forceinline__ void paged_join_of(const PagedArgs &a, const PagedCursor<R> &cur, const PagedItem &x, int c,
                                               uint32_t hi, uint32_t total) {
     PagedJoin j = {-1, x.row, x.token, x.head, x.left, x.g, {0, 0}};
     if (cur.end() > hi && !(x.part & 1)) j.last = -1;      // it was begun earlier
@@ -348,13 +345,15 @@ constexpr float kLazy = 8.f;
 
 // ------------------------------------------------------------------ rows at explicit positions
 
-// cos and sin of position * base^(-i/P): the turns in 64 bits, so that far positions keep
-// their angle (in fp32 position 10^6 would be off by 0.06 rad), less the whole ones, in fp32.
-__device__ __forceinline__ float2 paged_cos_sin(int32_t position, double turns) {
-    const double x = position * turns;
-    const float f = (float)(x - rint(x));
+// cos and sin of position * base^(-i/P).  A whole number of positions times the turns a position
+// (in units of 2^-64) modulo 2^64 is the fraction of a turn, exactly but for the turns' own
+// rounding, however far the position is (in fp32 position 10^6 would be off by 0.06 rad); its
+// upper 32 bits go on to fp32.
+__device__ __forceinline__ float2 paged_cos_sin(int32_t position, uint64_t turns) {
+    const uint32_t p = (uint32_t)position, low = (uint32_t)turns, high = (uint32_t)(turns >> 32);
+    const uint32_t part = __umulhi(p, low) + p * high - (position < 0 ? low : 0u);
     float2 cs;
-    sincospif(2.f * f, &cs.y, &cs.x);
+    sincospif((float)(int32_t)part * 4.656612873077393e-10f, &cs.y, &cs.x);  // half turns: 2^-31
     return cs;
 }
 
@@ -382,7 +381,7 @@ struct Row8 {
         }
     }
 
-    __device__ __forceinline__ void prologue(const double *turns, float eps, int e) {
+    __device__ __forceinline__ void prologue(const uint64_t *turns, float eps, int e) {
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) ss = fmaf(x[i].x, x[i].x, fmaf(x[i].y, x[i].y, ss));
@@ -421,20 +420,21 @@ __device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, const 
 // copies that are still in flight.  Barriers: full / empty of the STAGES page stages (base +
 // 8 i, base + 8 (STAGES + i)), and of the kItemRing items behind them.  here[i]: stage i holds
 // a page; an absent one holds no keys.
-template <int STAGES, int TILE, int KSTAGE, int STAGE>
+template <int R, int STAGES, int TILE, int KSTAGE, int STAGE>
 __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t ring, uint32_t bars, uint32_t item_bars, PagedItem *items,
                                            volatile int *here, volatile int *abort_flag) {
     const int lane = threadIdx.x & 31;
     auto full = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)i; };
     auto empty = [&](int i) -> uint32_t { return bars + 8u * (uint32_t)(STAGES + i); };
-    PagedCursor cur;
+    constexpr int D = TILE / (2 * kPage);
+    PagedCursor<R> cur;
     uint32_t lo, hi, total;
     int it = 0;
     bool ok = true, more = paged_locate(a, c, lo, hi, total, cur);
     if (!more) {
         // an empty stretch inside an item that others share: a piece without keys
         if (lane == 0) a.joins[c].last = -1;
-        for (int r = lane; r < a.rows; r += 32) paged_part(a, TILE / (2 * kPage), 2 * c)[a.rows * (TILE / (2 * kPage)) + r] = -INFINITY;
+        for (int r = lane; r < R; r += 32) paged_part(a, D, 2 * c)[R * D + r] = -INFINITY;
     }
     for (int n = 0; ok; ++n) {
         const int slot = n % kItemRing;

@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     __syncthreads();
 
     if (warp == kWarps) {
-        paged_fill<S, L::TILE, L::TILE, 2 * L::TILE>(a, c, sbase + L::OFF_RING, full(0), item_bars, items,
+        paged_fill<R, S, L::TILE, L::TILE, 2 * L::TILE>(a, c, sbase + L::OFF_RING, full(0), item_bars, items,
                                                      here, abort_flag);
         return;
     }

@@ -134,7 +134,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
     // scores among them): 128 x 56 + 384 x 152 = 65,536.
     if (warp < 4) regs_dec<56>();
     if (warp == 0) {
-        paged_fill<S, L::TILE, L::KSTAGE, L::STAGE>(a, c, sbase + L::OFF_RING, bar(L::B_FULL),
+        paged_fill<kRows, S, L::TILE, L::KSTAGE, L::STAGE>(a, c, sbase + L::OFF_RING, bar(L::B_FULL),
                                                     bar(L::B_ITEM), items, here, abort_flag);
     } else if (warp == 1) {
         // ------------------------------------------------ S = Q K^T
