@@ -236,7 +236,7 @@ int launch_copy(const CopyArgs &a, const PagedCache &c, const int32_t *pairs, in
 // and sums, a lane each, then O, eight lanes a piece, with the loads of 32 pieces on the way
 // at a time: three trips to memory whatever their number up to 32.
 
-constexpr int kJoinThreads = 512;
+constexpr int kJoinThreads = 256;
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a) {
@@ -314,7 +314,7 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
 template <int D, typename T>
 int launch_join(const PagedArgs &a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.shares, (unsigned)(a.rows <= 64 ? a.rows / 16 : 6));
+    cfg.gridDim = dim3((unsigned)a.shares, (unsigned)(a.rows <= 64 ? a.rows / 8 : 12));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};
