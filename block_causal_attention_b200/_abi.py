@@ -161,6 +161,17 @@ def lib() -> ctypes.CDLL:
     return _lib
 
 
+def paged_binding():
+    """The compiled calls of the paged cache (csrc/paged_binding.cpp)."""
+    lib()
+    try:
+        from . import _paged_binding
+    except ImportError as e:
+        raise ImportError(f"the module _paged_binding is not built for this PyTorch ({e}); run "
+                          "`python -m block_causal_attention_b200.build --force`") from e
+    return _paged_binding
+
+
 def error_string(code: int) -> str:
     return lib().bca_error_string(int(code)).decode()
 

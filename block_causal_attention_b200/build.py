@@ -1,4 +1,5 @@
-"""Build libbca.so (the C-ABI library) in-tree with nvcc for sm_100a."""
+"""Build libbca.so (the C-ABI library) in-tree with nvcc for sm_100a, and the Python module
+that calls its paged cache."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -11,6 +12,7 @@ ROOT = os.path.dirname(PKG)
 CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbca.so")
+BINDING = os.path.join(PKG, "_paged_binding.so")
 SOURCES = ["api.cpp", "plan.cpp", "fwd.cu", "fwd_static.cu", "bwd.cu", "cp_passes.cu", "paged_api.cpp", "paged.cu",
            "paged_rows.cu", "paged_tiles.cu"]
 HEADERS = ["plan.hpp", "kernels.hpp", "sm100.cuh", "prologue.cuh", "paged.hpp", "paged_device.cuh", "paged_mma.cuh"]
@@ -31,6 +33,21 @@ def _stale(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _binding_command(target: str) -> list:
+    """The Python module over torch tensors (csrc/paged_binding.cpp), against libbca.so."""
+    import sysconfig
+
+    import torch
+    from torch.utils import cpp_extension as ext
+    lib = os.path.join(os.path.dirname(torch.__file__), "lib")
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(_nvcc())))
+    inc = [f"-I{p}" for p in [*ext.include_paths(), sysconfig.get_path("include"), os.path.join(cuda, "include")]]
+    return [shutil.which("g++") or "g++", "-O2", "-std=c++17", "-fPIC", "-shared", "-w", *inc,
+            f"-D_GLIBCXX_USE_CXX11_ABI={int(torch._C._GLIBCXX_USE_CXX11_ABI)}",
+            os.path.join(CSRC, "paged_binding.cpp"), "-o", target, f"-L{PKG}", "-l:libbca.so", f"-L{lib}",
+            "-ltorch_python", "-ltorch_cpu", "-ltorch", "-lc10", "-lc10_cuda", "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
@@ -63,6 +80,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         tmp = LIB + f".tmp{os.getpid()}"
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lpthread"])
         os.replace(tmp, LIB)
+    header = os.path.join(ROOT, "include", "bca.h")
+    if force or _stale(BINDING, [os.path.join(CSRC, "paged_binding.cpp"), header]):
+        tmp = BINDING + f".tmp{os.getpid()}"
+        run(_binding_command(tmp))
+        os.replace(tmp, BINDING)
     return LIB
 
 

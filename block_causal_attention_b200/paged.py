@@ -52,7 +52,6 @@ class PagedCache:
         self.pool_bytes = int(self._lib.bca_paged_pool_bytes(self._h))
         self._pools: Dict[str, torch.Tensor] = {}
         self.device = None
-        self._o_dtype = torch.float32 if self.o_fp32 else dtype
         if self.host_only:
             return
         self.device = torch.device("cuda", torch.cuda.current_device())
@@ -60,11 +59,14 @@ class PagedCache:
                                    ("v_pages", v_pages, dtype, self.v_shape)):
             if t is None:
                 t = torch.empty(shape, dtype=dt, device=self.device)
-            else:
-                self._tensor(name, t, dt, shape)
+            elif t.dtype != dt or t.shape != shape or t.device != self.device or not t.is_contiguous():
+                raise ValueError(f"{name}: expected a contiguous {dt} tensor of shape {shape} on {self.device}, got "
+                                 f"{t.dtype} {tuple(t.shape)} on {t.device}")
             self._pools[name] = t
-        self._index = self.device.index
-        self._k_pool, self._v_pool = self.k_pages.data_ptr(), self.v_pages.data_ptr()
+        self._calls = _abi.paged_binding()
+        self._c = self._calls.cache(self._h.value, self.hq, self.hkv, self.d, self.layers, self.pool_bytes,
+                                    self.k_pages.data_ptr(), self.v_pages.data_ptr(), int(dtype == torch.float16),
+                                    int(self.o_fp32), self.device.index)
 
     @property
     def k_pages(self):
@@ -76,40 +78,16 @@ class PagedCache:
         """[layers][pages][Hkv][16][D][8], the cache's dtype."""
         return self._pools.get("v_pages")
 
-    # ------------------------------------------------------------------ arguments
-    # These run before every launch, so they are written for few interpreter steps.
-    def _tensor(self, name, t, dtype, shape):
-        if t.dtype is dtype and t.shape == shape and t.is_contiguous() and t.device == self.device:
-            return t.data_ptr()
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {shape} on {self.device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    def _on_gpu(self):
+        if self.host_only or not self._h.value:
+            raise _abi.BcaError(_abi.BCA_ERR_HOST_ONLY_PLAN if self.host_only else _abi.BCA_ERR_INVALID_ARGUMENT,
+                                "paged cache")
+        return self._c
 
-    def _prologue(self, rows, pos, gain, gain_name):
-        if pos is None:
-            if gain is not None:
-                raise ValueError(f"{gain_name} needs pos: rows without positions are taken as post-prologue")
-            return None, None
-        return (self._tensor("pos", pos, torch.int32, (rows, 3)),
-                None if gain is None else self._tensor(gain_name, gain, torch.float32, (self.d,)))
-
-    def _layer(self, layer):
-        if self.host_only:
-            raise _abi.BcaError(_abi.BCA_ERR_HOST_ONLY_PLAN, "paged cache")
-        if not 0 <= layer < self.layers:
-            raise ValueError(f"layer {layer} of {self.layers}")
-        at = layer * self.pool_bytes
-        return self._k_pool + at, self._v_pool + at
-
-    def _table(self, table):
-        shape = table.shape
-        if len(shape) != 2:
-            raise ValueError("table: expected int32 [seqs, width]")
-        return self._tensor("table", table, torch.int32, shape), shape[0], shape[1]
-
-    def _stream(self, stream):
-        if stream is None:
-            return torch.cuda.current_stream(self._index).cuda_stream
-        return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else stream
+    @staticmethod
+    def _stream(stream):
+        """None: the current stream of the cache's device."""
+        return stream if stream is None or isinstance(stream, int) else int(stream.cuda_stream)
 
     # ------------------------------------------------------------------ operators
     def write(self, k, v, table, off, start, *, pos=None, k_gain=None, layer: int = 0, stream=None) -> None:
@@ -118,16 +96,8 @@ class PagedCache:
         through QK-Norm (k_gain, or ones) and RoPE; without, they are given post-prologue.
         table, off, start, pos: int32 tensors on the cache's device, read when the kernel runs.
         A token that has no page is dropped and reported by ``status``."""
-        kp, vp = self._layer(layer)
-        n = k.shape[0]
-        shape = (n, self.hkv, self.d)
-        kq, vq = self._tensor("k", k, self.dtype, shape), self._tensor("v", v, self.dtype, shape)
-        tab, seqs, width = self._table(table)
-        o = self._tensor("off", off, torch.int32, (seqs + 1,))
-        s = self._tensor("start", start, torch.int32, (seqs,))
-        p, gain = self._prologue(n, pos, k_gain, "k_gain")
-        rc = self._lib.bca_paged_write(self._h, kq, vq, n, p, gain, tab, seqs, width, o, s, kp, vp,
-                                       self._stream(stream))
+        c = self._on_gpu()
+        rc = self._calls.write(c, k, v, table, off, start, pos, k_gain, layer, self._stream(stream))
         if rc:
             _abi.check(rc, "bca_paged_write")
 
@@ -135,18 +105,19 @@ class PagedCache:
         """Make page pairs[i, 1] a copy of page pairs[i, 0], in every layer.  pairs: [n, 2] on
         the host (a CPU tensor, an array or a list), read before the call returns.  A page may
         be written once, and none that is written may be read."""
-        if hasattr(pairs, "is_cuda") and pairs.is_cuda:
-            raise ValueError("pairs: expected host data")
-        pairs = np.asarray(pairs)
-        if pairs.size and (pairs.ndim != 2 or pairs.shape[1] != 2 or pairs.dtype.kind not in "iu"):
-            raise ValueError(f"pairs: expected whole numbers [n, 2], got {pairs.dtype} {pairs.shape}")
-        if pairs.dtype != np.int32:
+        c = self._on_gpu()
+        if not (isinstance(pairs, torch.Tensor) and pairs.dtype is torch.int32 and pairs.is_contiguous()):
+            if isinstance(pairs, torch.Tensor) and pairs.is_cuda:
+                raise ValueError("pairs: expected host data")
+            pairs = np.asarray(pairs)
+            if pairs.size == 0:
+                pairs = np.zeros((0, 2), np.int32)
+            if pairs.ndim != 2 or pairs.shape[1] != 2 or pairs.dtype.kind not in "iu":
+                raise ValueError(f"pairs: expected whole numbers [n, 2], got {pairs.dtype} {pairs.shape}")
             if pairs.size and (pairs.min() < 0 or pairs.max() >= self.pages):
                 raise _abi.BcaError(_abi.BCA_ERR_BAD_PAGE, "bca_paged_copy")
-            pairs = pairs.astype(np.int32)
-        pairs = np.ascontiguousarray(pairs)
-        kp, vp = self._layer(0)
-        rc = self._lib.bca_paged_copy(self._h, pairs.ctypes.data, len(pairs), kp, vp, self._stream(stream))
+            pairs = torch.from_numpy(np.ascontiguousarray(pairs, dtype=np.int32))
+        rc = self._calls.copy(c, pairs, self._stream(stream))
         if rc:
             _abi.check(rc, "bca_paged_copy")
 
@@ -160,37 +131,11 @@ class PagedCache:
 
         Returns o; rows that see no key are zero.  Rows outside every slice are left as they
         were in a given o (else uninitialised).  lse (fp32 [Hq, nq], optional) is filled in."""
-        kp, vp = self._layer(layer)
-        nq = q.shape[0]
-        qp = self._tensor("q", q, self.dtype, (nq, self.hq, self.d))
-        tab, seqs, width = self._table(table)
-        shape = off.shape
-        if len(shape) != 1 or shape[0] < 1:
-            raise ValueError("off: expected int32 [slices + 1]")
-        slices = shape[0] - 1
-        i32, per_slice = torch.int32, (slices,)
-        offp = self._tensor("off", off, i32, shape)
-        if seq is None and slices != seqs:
-            raise ValueError("seq=None needs as many slices as table rows")
-        sp = None if seq is None else self._tensor("seq", seq, i32, per_slice)
-        kb = self._tensor("k_begin", k_begin, i32, per_slice)
-        ke = self._tensor("k_end", k_end, i32, per_slice)
-        p, gain = self._prologue(nq, pos, q_gain, "q_gain")
-        if o is None:
-            o = torch.empty((nq, self.hq, self.d), dtype=self._o_dtype, device=self.device)
-            op = o.data_ptr()
-        else:
-            op = self._tensor("o", o, self._o_dtype, (nq, self.hq, self.d))
-        lp = None if lse is None else self._tensor("lse", lse, torch.float32, (self.hq, nq))
-        if workspace is None:
-            workspace = self.alloc_workspace(nq, slices, stream)
-        elif workspace.numel() * workspace.element_size() < self.workspace_bytes(nq, slices) or \
-                workspace.device != self.device or not workspace.is_contiguous():
-            raise ValueError(f"workspace: expected {self.workspace_bytes(nq, slices)} contiguous bytes on {self.device}")
-        rc = self._lib.bca_paged_attend(self._h, qp, nq, p, gain, kp, vp, tab, seqs, width, offp, sp, kb, ke, slices,
-                                        1 if causal else 0, op, lp, workspace.data_ptr(), self._stream(stream))
-        if rc:
-            _abi.check(rc, "bca_paged_attend")
+        c = self._on_gpu()
+        o = self._calls.attend(c, q, table, off, k_begin, k_end, seq, causal, pos, q_gain, layer, o, lse, workspace,
+                               self._stream(stream))
+        if isinstance(o, int):
+            _abi.check(o, "bca_paged_attend")
         return o
 
     def workspace_bytes(self, nq: int, slices: int) -> int:
@@ -200,17 +145,17 @@ class PagedCache:
         """Workspace of an ``attend`` call of these sizes, on its stream.  Calls that may overlap
         on the GPU (two streams, two captured graphs replayed side by side) need one each."""
         n = max(16, self.workspace_bytes(nq, slices))
-        if stream is None:
-            return torch.empty(n, dtype=torch.uint8, device=self.device)
-        if not hasattr(stream, "cuda_stream"):
-            stream = torch.cuda.ExternalStream(int(stream), device=self.device)
-        with torch.cuda.stream(stream):   # so that its next user is behind this call
+        if isinstance(stream, int):
+            stream = torch.cuda.ExternalStream(stream, device=self.device)
+        with torch.cuda.stream(stream):   # its next user is behind this call; None: the current one
             return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def status(self, stream=None) -> int:
         """Status of the work on `stream`, waited for: BCA_OK, BCA_ERR_DEVICE_TIMEOUT, or
         BCA_ERR_BAD_PAGE when a written token had no page.  Reading it clears it."""
-        return int(self._lib.bca_paged_status(self._h, None if self.host_only else self._stream(stream)))
+        if stream is None and not self.host_only:
+            stream = torch.cuda.current_stream(self.device)
+        return int(self._lib.bca_paged_status(self._h, self._stream(stream)))
 
     def close(self) -> None:
         if getattr(self, "_h", None) is not None and self._h.value:

@@ -5,7 +5,7 @@ import pytest
 import torch
 
 import paged_ref as ref
-from block_causal_attention_b200 import PagedCache, _abi
+from block_causal_attention_b200 import BcaError, PagedCache, _abi
 
 pytestmark = pytest.mark.gpu
 PAGE = 128
@@ -387,3 +387,70 @@ def test_forced_timeout_is_reported_and_the_context_stays_usable(rows):
     assert good.status() == _abi.BCA_OK
     wo, _, bo, _ = ref.attend(q, kp[0], vp[0], table, [0, rows], [0], [0], [512], False)
     no_worse(o, wo, bo, "o")
+
+
+def test_refusals_of_the_binding():
+    g = gen(16)
+    cache = PagedCache(4, 2, 48, 6, layers=2)
+    k = rand((5, 2, 48), BF, g)
+    q = rand((5, 4, 48), BF, g)
+    table, off, one, pos = ref.i32([[0, 1]]), ref.i32([0, 5]), ref.i32([5]), positions(5, g)
+    gain = torch.ones(48, device="cuda")
+    good = dict(k=k, v=k, table=table, off=off, start=ref.i32([0]), pos=pos, k_gain=gain)
+    cache.write(**good)
+    for bad in (dict(k=k.half()), dict(v=k[:4]), dict(k=k.cpu()), dict(table=table[0]), dict(table=table.long()),
+                dict(off=off[:1]), dict(off=off.cpu()), dict(start=off), dict(pos=pos[:, :2]), dict(pos=None),
+                dict(k_gain=gain.half()), dict(k_gain=gain[:47]), dict(layer=2), dict(layer=-1),
+                dict(k=rand((2, 5, 48), BF, g).transpose(0, 1))):
+        with pytest.raises(ValueError):
+            cache.write(**{**good, **bad})
+    with pytest.raises(TypeError):
+        cache.write(**{**good, "k": None})
+    good = dict(q=q, table=table, off=off, k_begin=ref.i32([0]), k_end=one, seq=ref.i32([0]), pos=pos, q_gain=gain)
+    o = cache.attend(**good)
+    assert o.dtype is BF and o.shape == (5, 4, 48)
+    small = torch.empty(cache.workspace_bytes(5, 1) - 1, dtype=torch.uint8, device="cuda")
+    for bad in (dict(q=q.half()), dict(q=q[:, :3]), dict(q=q[:4]), dict(table=table.cpu()), dict(off=off.long()),
+                dict(k_begin=off), dict(k_end=one.cpu()), dict(seq=off), dict(pos=None), dict(q_gain=gain.double()),
+                dict(o=o.float()), dict(o=o[:3]), dict(lse=torch.empty(4, 4, device="cuda")), dict(workspace=small),
+                dict(workspace=small.cpu()), dict(layer=2), dict(off=off[:0]),
+                dict(table=ref.i32([[0, 1], [2, 3]]), seq=None)):
+        with pytest.raises(ValueError):
+            cache.attend(**{**good, **bad})
+    for bad in ([[0, 6]], [[-1, 0]], [[0, 1], [2, 1]], [[0, 1], [1, 2]], torch.tensor([[0, 1], [1, 2]])):
+        with pytest.raises(BcaError) as e:
+            cache.copy_pages(bad)
+        assert e.value.code == _abi.BCA_ERR_BAD_PAGE
+    for bad in (torch.zeros((1, 2), dtype=torch.int32, device="cuda"), [[0, 1, 2]], [0, 1], [[0.0, 1.0]]):
+        with pytest.raises(ValueError):
+            cache.copy_pages(bad)
+    cache.copy_pages([])
+    with pytest.raises(ValueError):
+        PagedCache(4, 2, 48, 6, k_pages=cache.k_pages)       # of a cache with another shape
+    # nothing to do is no error
+    assert cache.attend(q[:0], table, ref.i32([0, 0]), ref.i32([0]), one).shape == (0, 4, 48)
+    cache.write(k[:0], k[:0], table, ref.i32([0, 0]), ref.i32([0]))
+    cache.close()
+    for call in (lambda: cache.attend(**good), lambda: cache.copy_pages([])):
+        with pytest.raises(BcaError):
+            call()
+
+
+def test_allocations_of_a_call_on_another_stream_belong_to_it():
+    """Calls on a side stream while the current one keeps reusing freed memory."""
+    g = gen(17)
+    kp, vp = ref.pools(40, 1, 48, BF, g)
+    cache = PagedCache(16, 1, 48, 40, k_pages=kp, v_pages=vp)
+    table = ref.table_of([40], 40, g)
+    q = rand((2, 16, 48), BF, g)
+    args = (q, table, ref.i32([0, 2]), ref.i32([0]), ref.i32([5001]))
+    want = cache.attend(*args, causal=True)
+    torch.cuda.synchronize()
+    side = torch.cuda.Stream()
+    got = []
+    for _ in range(20):
+        got.append(cache.attend(*args, causal=True, stream=side))
+        for _ in range(3):
+            torch.full((cache.workspace_bytes(2, 1),), 255, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert all(torch.equal(x, want) for x in got)

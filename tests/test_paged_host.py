@@ -69,6 +69,10 @@ def test_null_arguments_and_a_host_only_cache():
         rc = L.bca_paged_attend(c._h, None, a["nq"], *[None] * 5, a["seqs"], a["width"], *[None] * 4, a["slices"], 0,
                                 *[None] * 4)
         assert rc == _abi.BCA_ERR_INVALID_ARGUMENT, bad
+    for call in (lambda: c.copy_pages([[0, 1]]), lambda: c.write(*[None] * 5), lambda: c.attend(*[None] * 5)):
+        with pytest.raises(BcaError) as e:
+            call()
+        assert e.value.code == _abi.BCA_ERR_HOST_ONLY_PLAN
     with pytest.raises(BcaError) as e:
         c.copy_pages([[0, 1]])
     assert e.value.code == _abi.BCA_ERR_HOST_ONLY_PLAN
