@@ -19,15 +19,18 @@ namespace {
 // k_hat = R(pos) (gain * k / sqrt(mean k^2 + eps)) in fp16, v as it is, both into the layout
 // of the pages.  Bound by memory: 4 D Hkv bytes read and as many written a token.
 //
-// A block takes the (up to) 32 tokens of one 32-aligned stretch of a page, all KV heads: the
-// angles (64-bit turns, sine and cosine) are computed once a token instead of once a head.
-// Eight lanes share a key row (one 16-byte chunk each, D / 8 of them at work), four
-// neighbouring tokens a warp, so that the stores of a chunk are 64 contiguous bytes.  A value
-// is written as the 16 bytes of eight neighbouring tokens (a whole row of the V layout) where
-// the call has all eight, else as single values: the other slots are not this call's.
+// A block takes the (up to) 32 tokens of one 32-aligned stretch of a page and up to eight KV
+// heads.  Their rows come to shared memory by bulk copies, one a token, issued before anything
+// else is computed: 50 KB on the way a block, four blocks a multiprocessor.  The angles (fixed
+// point, sine and cosine) are computed once a token for all heads.  Keys: a warp has a head, a
+// lane a token, so that the stores of a 16-byte chunk are 512 contiguous bytes.  Values: 8 x 8
+// matrices turned by ldmatrix.trans; two tokens of a channel a lane, 128 contiguous bytes a
+// store, and the pieces of a group of eight tokens that are not this call's are left out.
+// Rows of an odd number of 16-byte units keep both from bank conflicts.
 
 constexpr int kWriteTokens = 32;
 constexpr int kWriteThreads = 256;
+constexpr int kWriteHeads = 8;
 
 struct WriteArgs {
     const void *k, *v;
@@ -40,6 +43,7 @@ struct WriteArgs {
     int64_t n, pages;
     int seqs, width, hkv;
     float eps;
+    uint64_t timeout_ns;
     uint64_t turns[24];
 };
 
@@ -77,13 +81,31 @@ __device__ __forceinline__ bool write_tile(const WriteArgs &a, WriteTile &t) {
     return true;
 }
 
+template <int D>
+struct WriteSmem {
+    static constexpr int STRIDE = kWriteHeads * D * 2 + 16;  // bytes of a token; 16 times an odd number
+    static constexpr int OFF_V = kWriteTokens * STRIDE;
+    static constexpr int OFF_TURN = 2 * OFF_V;               // cos, sin [pair][token]
+    static constexpr int OFF_GAIN = OFF_TURN + D / 2 * kWriteTokens * 8;
+    static constexpr int OFF_BAR = OFF_GAIN + D * 4;
+    static constexpr int BYTES = OFF_BAR + 8;
+};
+
 template <int D, typename T>
 __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const __grid_constant__ WriteArgs a) {
+    using L = WriteSmem<D>;
     constexpr int P = Geo<D>::PAIRS;
     constexpr int C = D / 8;
-    __shared__ float2 turn[kWriteTokens][3 * P];
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t sbase = sm100::smem_u32(smem), bar = sbase + L::OFF_BAR;
+    float2 *turn = reinterpret_cast<float2 *>(smem + L::OFF_TURN);
+    float *gain = reinterpret_cast<float *>(smem + L::OFF_GAIN);
+    if (threadIdx.x == 0) {
+        sm100::mbar_init(bar, 1);
+        sm100::mbar_fence_init();
+    }
     WriteTile t;
-    if (!write_tile(a, t)) return;
+    if (!write_tile(a, t)) return;  // its barriers are also the one behind mbar_init
     const int64_t page_at = t.at / kPage;
     int64_t page = -1;
     if (t.at >= 0 && page_at < a.width) page = __ldg(a.table + (int64_t)t.b * a.width + page_at);
@@ -91,93 +113,116 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const __grid
         if (threadIdx.x == 0) atomicOr(a.status, kPagedNoPage);
         return;
     }
-    const int slot = (int)(t.at % kPage);
-    if (a.pos) {
-        for (int u = threadIdx.x; u < t.count * 3 * P; u += kWriteThreads) {
-            const int tok = u / (3 * P), p = u % (3 * P), axis = p / P;
-            turn[tok][p] = paged_cos_sin(__ldg(a.pos + (t.row + tok) * 3 + axis), a.turns[8 * axis + p - axis * P]);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int first = (int)(t.at % kWriteTokens), slot0 = (int)(t.at % kPage) - first;  // token i of the stretch: row i
+    const int h0 = blockIdx.y * kWriteHeads, heads = min(kWriteHeads, a.hkv - h0);
+    const bool mine = lane >= first && lane < first + t.count;
+    const int64_t row = t.row + lane - first;
+    if (warp == 0) {
+        const uint32_t bytes = heads * D * 2;
+        if (lane == 0) sm100::mbar_arrive_expect_tx(bar, 2 * t.count * bytes);
+        __syncwarp();
+        if (mine) {
+            const int64_t at = (row * a.hkv + h0) * D;
+            sm100::bulk_g2s(sbase + lane * L::STRIDE, static_cast<const T *>(a.k) + at, bytes, bar);
+            sm100::bulk_g2s(sbase + L::OFF_V + lane * L::STRIDE, static_cast<const T *>(a.v) + at, bytes, bar);
         }
+    }
+    if (a.pos) {
+#pragma unroll 1
+        for (int p = warp; p < D / 2; p += kWriteThreads / 32)
+            if (mine)
+                turn[p * kWriteTokens + lane] =
+                    p < 3 * P ? paged_cos_sin(__ldg(a.pos + row * 3 + p / P), a.turns[8 * (p / P) + p % P])
+                              : make_float2(1.f, 0.f);
+        if (threadIdx.x < D) gain[threadIdx.x] = a.k_gain ? __ldg(a.k_gain + threadIdx.x) : 1.f;
         __syncthreads();
     }
-
-    // keys
-    const T *k = static_cast<const T *>(a.k);
-    const int fours = (t.count + 3) / 4;
-    const int e = threadIdx.x % 8;
-    float gain[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) gain[i] = a.k_gain && e < C ? __ldg(a.k_gain + 8 * e + i) : 1.f;
-    for (int u = threadIdx.x / 8; u < fours * a.hkv * 4; u += kWriteThreads / 8) {
-        const int head = u / 4 % a.hkv, tok = u / 4 / a.hkv * 4 + u % 4;
-        const bool on = tok < t.count && e < C;
-        float x[8];
-        uint4 raw = make_uint4(0, 0, 0, 0);
-        if (on) raw = __ldg(reinterpret_cast<const uint4 *>(k + ((t.row + tok) * a.hkv + head) * D) + e);
-        const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = Io<T>::unpack(w[i]);
-            x[2 * i] = f.x;
-            x[2 * i + 1] = f.y;
-        }
-        if (a.pos) {
-            float ss = 0.f;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) ss = fmaf(x[i], x[i], ss);
-#pragma unroll
-            for (int o = 4; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffu << (threadIdx.x & 24), ss, o);
-            const float r = rsqrtf(ss * (1.0f / D) + a.eps);
-            if (on) {
-#pragma unroll
-                for (int i = 0; i < 8; ++i) x[i] = x[i] * r * gain[i];
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    const int p = 4 * e + i;
-                    if (p < 3 * P) {
-                        const float2 cs = turn[tok][p];
-                        const float y0 = x[2 * i], y1 = x[2 * i + 1];
-                        x[2 * i] = y0 * cs.x - y1 * cs.y;
-                        x[2 * i + 1] = y0 * cs.y + y1 * cs.x;
-                    }
-                }
-            }
-        }
-        if (on)
-            *reinterpret_cast<uint4 *>(a.k_pages + (((page * a.hkv + head) * C + e) * kPage + slot + tok) * 8) =
-                make_uint4(sm100::pack_f16x2(x[0], x[1]), sm100::pack_f16x2(x[2], x[3]),
-                           sm100::pack_f16x2(x[4], x[5]), sm100::pack_f16x2(x[6], x[7]));
+    if (!sm100::mbar_wait(bar, 0, a.timeout_ns)) {
+        if (threadIdx.x == 0) atomicOr(a.status, kPagedTimeout);
+        sm100::mbar_wait(bar, 0, a.timeout_ns);  // the copies' memory must not be given back before they land
+        return;
     }
 
-    // values: a thread turns eight tokens x two channels
-    const uint32_t *v = static_cast<const uint32_t *>(a.v);
-    uint16_t *vp = static_cast<uint16_t *>(a.v_pages);
-    const int g0 = slot / 8, groups = (slot + t.count - 1) / 8 - g0 + 1;
-    for (int u = threadIdx.x; u < groups * a.hkv * (D / 2); u += kWriteThreads) {
-        const int p = u % (D / 2), head = u / (D / 2) % a.hkv, grp = g0 + u / (D / 2) / a.hkv;
-        uint32_t w[8];
-        const int tok0 = grp * 8 - slot;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const int tok = tok0 + i;
-            w[i] = tok >= 0 && tok < t.count ? __ldg(v + ((t.row + tok) * a.hkv + head) * (D / 2) + p) : 0u;
-        }
-        uint16_t *dst = vp + (((page * a.hkv + head) * 16 + grp) * D + 2 * p) * 8;
-        if (tok0 >= 0 && tok0 + 8 <= t.count) {
-            uint32_t lo[4], hi[4];
+    if (warp >= heads) return;
+
+    // keys: twice over the row in shared memory, so that the code stays short (a call of few tokens
+    // takes as long as its instructions take to come)
+    if (mine) {
+        const uint4 *src = reinterpret_cast<const uint4 *>(smem + lane * L::STRIDE + warp * D * 2);
+        uint4 *dst = reinterpret_cast<uint4 *>(a.k_pages) + (page * a.hkv + h0 + warp) * C * kPage + slot0 + lane;
+        auto chunk = [&](int c, float (&x)[8]) {
+            const uint4 raw = src[c];
+            const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                lo[i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x5410);
-                hi[i] = __byte_perm(w[2 * i], w[2 * i + 1], 0x7632);
+                const float2 f = Io<T>::unpack(w[i]);
+                x[2 * i] = f.x;
+                x[2 * i + 1] = f.y;
             }
-            reinterpret_cast<uint4 *>(dst)[0] = make_uint4(lo[0], lo[1], lo[2], lo[3]);
-            reinterpret_cast<uint4 *>(dst)[1] = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        } else {
+        };
+        float r = 1.f;
+        if (a.pos) {
+            float ss[2] = {0.f, 0.f};
 #pragma unroll
-            for (int i = 0; i < 8; ++i) {
-                const int tok = tok0 + i;
-                if (tok < 0 || tok >= t.count) continue;
-                dst[i] = (uint16_t)w[i];
-                dst[8 + i] = (uint16_t)(w[i] >> 16);
+            for (int c = 0; c < C; ++c) {
+                float x[8];
+                chunk(c, x);
+#pragma unroll
+                for (int i = 0; i < 8; ++i) ss[i & 1] = fmaf(x[i], x[i], ss[i & 1]);
+            }
+            r = rsqrtf((ss[0] + ss[1]) * (1.0f / D) + a.eps);
+        }
+#pragma unroll 2
+        for (int c = 0; c < C; ++c) {
+            float x[8];
+            chunk(c, x);
+            if (a.pos) {
+                const float4 *gn = reinterpret_cast<const float4 *>(gain) + 2 * c;
+                const float g[8] = {gn[0].x, gn[0].y, gn[0].z, gn[0].w, gn[1].x, gn[1].y, gn[1].z, gn[1].w};
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const float2 cs = turn[(4 * c + i) * kWriteTokens + lane];
+                    const float y0 = x[2 * i] * r * g[2 * i], y1 = x[2 * i + 1] * r * g[2 * i + 1];
+                    x[2 * i] = y0 * cs.x - y1 * cs.y;
+                    x[2 * i + 1] = y0 * cs.y + y1 * cs.x;
+                }
+            }
+            dst[c * kPage] = make_uint4(sm100::pack_f16x2(x[0], x[1]), sm100::pack_f16x2(x[2], x[3]),
+                                        sm100::pack_f16x2(x[4], x[5]), sm100::pack_f16x2(x[6], x[7]));
+        }
+    }
+    __syncwarp();
+
+    // values: the four groups of eight tokens of eight channels at a time; the lane gets channel
+    // lane / 4, tokens 2 (lane % 4) and the next of each
+    const uint32_t from = sbase + L::OFF_V + lane * L::STRIDE + warp * D * 2;
+    uint16_t *dst = static_cast<uint16_t *>(a.v_pages) +
+                    (((page * a.hkv + h0 + warp) * 16 + slot0 / 8) * D + lane / 4) * 8 + 2 * (lane % 4);
+    uint32_t have = 0;  // bits 2 k, 2 k + 1: the lane's two tokens of group k are this call's
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int i = 8 * k + 2 * (lane % 4) + j;
+            have |= (uint32_t)(i >= first && i < first + t.count) << (2 * k + j);
+        }
+#pragma unroll 2
+    for (int c = 0; c < C; ++c) {
+        uint32_t r[4];
+        asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                     : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                     : "r"(from + c * 16)
+                     : "memory");
+#pragma unroll
+        for (int k = 0; k < 4; ++k) {
+            uint16_t *to = dst + (k * D + c * 8) * 8;
+            const uint32_t both = have >> (2 * k) & 3u;
+            if (both == 3u) {
+                *reinterpret_cast<uint32_t *>(to) = r[k];
+            } else {
+                if (both & 1u) to[0] = (uint16_t)r[k];
+                if (both & 2u) to[1] = (uint16_t)(r[k] >> 16);
             }
         }
     }
@@ -355,7 +400,15 @@ size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices) {
 }
 
 int prepare_paged(const PagedCache &c) {
-    const int rc = prepare_paged_rows(c);
+    int rc = by_type(c, [](auto d, auto t) {
+        using L = WriteSmem<decltype(d)::value>;
+        return cudaFuncSetAttribute(paged_write_kernel<decltype(d)::value, decltype(t)>,
+                                    cudaFuncAttributeMaxDynamicSharedMemorySize, L::BYTES) == cudaSuccess
+                   ? BCA_OK
+                   : BCA_ERR_CUDA;
+    });
+    if (rc != BCA_OK) return rc;
+    rc = prepare_paged_rows(c);
     return rc == BCA_OK ? prepare_paged_tiles(c) : rc;
 }
 
@@ -377,11 +430,14 @@ int launch_paged_write(const PagedCache &c, const PagedWriteIO &io, cudaStream_t
     a.width = io.width;
     a.hkv = c.hkv;
     a.eps = c.eps;
+    a.timeout_ns = kPagedWaitNs;
     std::memcpy(a.turns, c.turns, sizeof(a.turns));
     const int64_t blocks = io.n / kWriteTokens + 2 * (int64_t)io.seqs;
     if (blocks > INT32_MAX) return BCA_ERR_TOO_LARGE;
     return by_type(c, [&](auto d, auto t) {
-        paged_write_kernel<decltype(d)::value, decltype(t)><<<(unsigned)blocks, kWriteThreads, 0, stream>>>(a);
+        const dim3 grid((unsigned)blocks, (unsigned)((c.hkv + kWriteHeads - 1) / kWriteHeads));
+        paged_write_kernel<decltype(d)::value, decltype(t)>
+            <<<grid, kWriteThreads, WriteSmem<decltype(d)::value>::BYTES, stream>>>(a);
         return cudaGetLastError() == cudaSuccess ? BCA_OK : BCA_ERR_CUDA;
     });
 }
