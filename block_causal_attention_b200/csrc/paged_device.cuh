@@ -405,11 +405,24 @@ struct Row8 {
 
 constexpr uint64_t kPagedWaitNs = 2000000000ull;  // a healthy wait is microseconds
 
+// A thread that finds the phase incomplete asks to be put to sleep for up to 20 us at a time:
+// two warps that poll take issue slots from the softmax warps beside them (2 % of paged_tiles).
 __device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, const PagedArgs &a,
                                            volatile int *abort_flag) {
     if (sm100::mbar_try_wait(bar, parity)) return true;
     if (*abort_flag) return false;
-    if (sm100::mbar_wait(bar, parity, a.timeout_ns)) return true;
+    const uint64_t t0 = sm100::globaltimer_ns();
+    do {
+        uint32_t done;
+        asm volatile(
+            "{\n\t.reg .pred p;\n\t"
+            "mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+            "selp.u32 %0, 1, 0, p;\n\t}"
+            : "=r"(done)
+            : "r"(bar), "r"(parity), "r"(20000u)
+            : "memory");
+        if (done) return true;
+    } while (sm100::globaltimer_ns() - t0 < a.timeout_ns);
     atomicOr(a.status, kPagedTimeout);
     *abort_flag = 1;
     return false;

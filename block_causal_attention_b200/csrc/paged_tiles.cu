@@ -316,25 +316,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
             };
             // A step in which every row sees every key.  The maxima are not looked at: weights may
             // grow to kTop before the reference has to move, and their sums, which are needed
-            // anyway, tell.  Half of the step before's P V products stand between its exponentials
-            // (the other half has covered the way of its scores from tensor memory), so that a warp
-            // alone keeps both units at work.  False, with s still to be had from tensor
+            // anyway, tell.  The P V products of the step before stand between its exponentials, so
+            // that a warp alone keeps both units at work.  False, with s still to be had from tensor
             // memory, if the reference has to move.
             auto fast_step = [&](bool before, uint32_t vs, int vstep) {
                 uint32_t pn[2][kTiles / 2][4];
                 float2 add[2][2];
-                uint32_t vf[NV][2];
-                if (before) ldsm_v<NV>(vs + (vstep * kTiles + 2) * (D * 16) + vaddr, vf);
 #pragma unroll
-                for (int k = 0; k < kChunk / 16; ++k)
+                for (int k = 0; k < kChunk / 16; ++k) {
+                    uint32_t vf[NV][2];
+                    if (before) ldsm_v<NV>(vs + (vstep * kTiles + 2 * k) * (D * 16) + vaddr, vf);
 #pragma unroll
                     for (int m = 0; m < 2; ++m) {
                         weights(m, k, pn[m][k], add[m]);
                         if (before)
 #pragma unroll
-                            for (int n = k * NV / 2; n < (k + 1) * NV / 2; ++n)
-                                mma16<Io<T>::kF16>(o[m][n], pa[m][1], vf[n][0], vf[n][1]);
+                            for (int n = 0; n < NV; ++n) mma16<Io<T>::kF16>(o[m][n], pa[m][k], vf[n][0], vf[n][1]);
                     }
+                }
                 bool high = false;
                 float row[2][2];
 #pragma unroll
@@ -379,14 +378,12 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                         for (;;) {
                             const uint32_t vs = page_v(it % S);
                             load_s(1);
-                            products(vs, 0, 0);
 #pragma unroll
                             for (step = 1; step < kSteps; ++step) {
                                 wait_s();
                                 if (!fast_step(true, vs, step - 1)) break;
                                 if (step + 1 < kSteps) {
                                     load_s(step + 1);
-                                    products(vs, step, 0);
                                 } else {
                                     free_s();
                                 }
@@ -404,13 +401,13 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                             if (!wait_page()) break;
                             on = here[it % S];
                             step = 0;
-                            if (on) load_s(0);
-                            products(vs, kSteps - 1, 0);
                             if (!on) {
+                                products(vs, kSteps - 1, 0);
                                 products(vs, kSteps - 1, 1);
                                 free_page(old);
                                 break;
                             }
+                            load_s(0);
                             wait_s();
                             const bool go = fast_step(true, vs, kSteps - 1);
                             free_page(old);
