@@ -324,6 +324,12 @@ struct Io<__nv_bfloat16> {
     }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return sm100::pack_bf16x2(lo, hi); }
     static __device__ __forceinline__ bool bad(uint32_t bits) { return (bits & 0x7f80u) == 0x7f80u; }
+    // sum + 0 v in both halves: +-0 as long as every v was finite
+    static __device__ __forceinline__ uint32_t add_zero_times(uint32_t v, uint32_t sum) {
+        const __nv_bfloat162 r = __hfma2(*reinterpret_cast<const __nv_bfloat162 *>(&v), __floats2bfloat162_rn(0.f, 0.f),
+                                         *reinterpret_cast<const __nv_bfloat162 *>(&sum));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
 };
 template <>
 struct Io<__half> {
@@ -338,6 +344,11 @@ struct Io<__half> {
     }
     static __device__ __forceinline__ uint32_t pack(float lo, float hi) { return sm100::pack_f16x2(lo, hi); }
     static __device__ __forceinline__ bool bad(uint32_t bits) { return (bits & 0x7c00u) == 0x7c00u; }
+    static __device__ __forceinline__ uint32_t add_zero_times(uint32_t v, uint32_t sum) {
+        const __half2 r = __hfma2(*reinterpret_cast<const __half2 *>(&v), __floats2half2_rn(0.f, 0.f),
+                                  *reinterpret_cast<const __half2 *>(&sum));
+        return *reinterpret_cast<const uint32_t *>(&r);
+    }
 };
 
 // The reference moves when a score passes it by more than this (in powers of two).
@@ -349,39 +360,53 @@ constexpr float kLazy = 8.f;
 // (in units of 2^-64) modulo 2^64 is the fraction of a turn, exactly but for the turns' own
 // rounding, however far the position is (in fp32 position 10^6 would be off by 0.06 rad); its
 // upper 32 bits go on to fp32.
-__device__ __forceinline__ float2 paged_cos_sin(int32_t position, uint64_t turns) {
+__device__ __forceinline__ int32_t paged_turn(int32_t position, uint64_t turns) {
     const uint32_t p = (uint32_t)position, low = (uint32_t)turns, high = (uint32_t)(turns >> 32);
-    const uint32_t part = __umulhi(p, low) + p * high - (position < 0 ? low : 0u);
+    return (int32_t)(__umulhi(p, low) + p * high - (position < 0 ? low : 0u));  // in units of 2^-32
+}
+__device__ __forceinline__ float2 paged_cos_sin(int32_t position, uint64_t turns) {
     float2 cs;
-    sincospif((float)(int32_t)part * 4.656612873077393e-10f, &cs.y, &cs.x);  // half turns: 2^-31
+    sincospif((float)paged_turn(position, turns) * 4.656612873077393e-10f, &cs.y, &cs.x);  // half turns: 2^-31
     return cs;
+}
+// The same from the special-function unit, for queries: they are rounded to fp16 (2^-12 of a
+// value) and used once, so an error of 2^-20 does not count, while the queries of an item are
+// 9,216 angles that stand before its first score (they took 6 us of every block's life).
+__device__ __forceinline__ float2 paged_cos_sin_fast(int32_t position, uint64_t turns) {
+    const float x = (float)paged_turn(position, turns) * 1.4629180792671596e-9f;  // radians: 2 pi 2^-32
+    return make_float2(__cosf(x), __sinf(x));
 }
 
 // What eight lanes make of a row: lane e has channel pairs e, e + 8, e + 16 (those below
-// D / 2).  x: the raw values in, QK-Norm and RoPE applied out.
+// D / 2).
 template <int D>
 struct Row8 {
     static constexpr int P = Geo<D>::PAIRS;
     static constexpr int N = (D / 2 + 7) / 8;
     float2 x[N];
-
-    float2 gn[N];
     int32_t at[N];
 
-    // Everything that the row needs from memory, on the way at the same time.
+    // The raw values and the positions, on the way at the same time.
     template <typename T>
-    __device__ __forceinline__ void load(const T *row, const int32_t *pos, const float *gain, int e) {
+    __device__ __forceinline__ void load(const T *row, const int32_t *pos, int e) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
             const int p = e + 8 * i;
             x[i] = p < D / 2 ? Io<T>::unpack(__ldg(reinterpret_cast<const uint32_t *>(row) + p)) : float2{0.f, 0.f};
             at[i] = pos && p < 3 * P ? __ldg(pos + p / P) : 0;
-            gn[i] = pos && gain && p < D / 2 ? make_float2(__ldg(gain + 2 * p), __ldg(gain + 2 * p + 1))
-                                             : make_float2(1.f, 1.f);
         }
     }
-
-    __device__ __forceinline__ void prologue(const uint64_t *turns, float eps, int e) {
+    // The lane's part of the QK-Norm gain.
+    static __device__ __forceinline__ void load_gain(const float *gain, int e, float2 (&gn)[N]) {
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const int p = e + 8 * i;
+            gn[i] = gain && p < D / 2 ? make_float2(__ldg(gain + 2 * p), __ldg(gain + 2 * p + 1))
+                                      : make_float2(1.f, 1.f);
+        }
+    }
+    // QK-Norm and RoPE.
+    __device__ __forceinline__ void prologue(const float2 (&gn)[N], const uint64_t *turns, float eps, int e) {
         float ss = 0.f;
 #pragma unroll
         for (int i = 0; i < N; ++i) ss = fmaf(x[i].x, x[i].x, fmaf(x[i].y, x[i].y, ss));
@@ -394,7 +419,7 @@ struct Row8 {
             const float y0 = x[i].x * r * gn[i].x, y1 = x[i].y * r * gn[i].y;
             x[i] = make_float2(y0, y1);
             if (p < 3 * P) {
-                const float2 cs = paged_cos_sin(at[i], turns[8 * (p / P) + p % P]);
+                const float2 cs = paged_cos_sin_fast(at[i], turns[8 * (p / P) + p % P]);
                 x[i] = make_float2(y0 * cs.x - y1 * cs.y, y0 * cs.y + y1 * cs.x);
             }
         }
@@ -443,30 +468,46 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
     PagedCursor<R> cur;
     uint32_t lo, hi, total;
     int it = 0;
-    bool ok = true, more = paged_locate(a, c, lo, hi, total, cur);
+    bool more = paged_locate(a, c, lo, hi, total, cur);
     if (!more) {
         // an empty stretch inside an item that others share: a piece without keys
         if (lane == 0) a.joins[c].last = -1;
         for (int r = lane; r < R; r += 32) paged_part(a, D, 2 * c)[R * D + r] = -INFINITY;
     }
-    for (int n = 0; ok; ++n) {
-        const int slot = n % kItemRing;
-        if (n >= kItemRing)
-            ok = __all_sync(0xffffffffu, paged_wait(item_bars + 8u * (uint32_t)(kItemRing + slot),
-                                                    (n / kItemRing - 1) & 1, a, abort_flag));
-        if (!ok) break;
-        PagedItem x;
-        if (more) paged_item(a, cur, c, lo, hi, x);
-        else x.p0 = -1;
+    // An item is published before the pages of the one before it are loaded, so that its queries
+    // can be made ready meanwhile.
+    int published = 0;
+    PagedItem x;
+    const int32_t *row = nullptr;
+    auto publish = [&] {
+        const int slot = published % kItemRing;
+        if (published >= kItemRing &&
+            !__all_sync(0xffffffffu, paged_wait(item_bars + 8u * (uint32_t)(kItemRing + slot),
+                                                (published / kItemRing - 1) & 1, a, abort_flag)))
+            return false;
+        if (more) {
+            paged_item(a, cur, c, lo, hi, x);
+            row = a.table + (int64_t)cur.s.b * a.width;
+            if (lane == 0 && cur.end() >= hi) paged_join_of(a, cur, x, c, hi, total);
+        } else {
+            x.p0 = -1;
+        }
         if (lane == 0) {
             items[slot] = x;
             sm100::mbar_arrive(item_bars + 8u * (uint32_t)slot);
         }
-        if (!more) break;
-        const int32_t *row = a.table + (int64_t)cur.s.b * a.width;
-        for (int32_t base = x.p0; base < x.p1 && ok && !a.skip_loads; base += 32) {
-            const int32_t mine = base + lane < x.p1 ? __ldg(row + base + lane) : -1;
-            const int count = min(32, x.p1 - base);
+        ++published;
+        return true;
+    };
+    bool ok = publish();
+    while (ok && more) {
+        const int32_t p0 = x.p0, p1 = x.p1, g = x.g;
+        const int32_t *pages = row;
+        more = cur.end() < hi && cur.next(a);
+        ok = publish();
+        for (int32_t base = p0; base < p1 && ok && !a.skip_loads; base += 32) {
+            const int32_t mine = base + lane < p1 ? __ldg(pages + base + lane) : -1;
+            const int count = min(32, p1 - base);
             for (int j = 0; j < count; ++j) {
                 const int32_t page = __shfl_sync(0xffffffffu, mine, j);
                 if (lane == 0 && ok) {
@@ -476,7 +517,7 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
                         const bool on = page >= 0 && page < a.pages;
                         here[st] = on;
                         if (on) {
-                            const int64_t at = ((int64_t)page * a.hkv + x.g) * TILE;
+                            const int64_t at = ((int64_t)page * a.hkv + g) * TILE;
                             const uint32_t dst = ring + st * STAGE;
                             sm100::mbar_arrive_expect_tx(full(st), 2 * TILE);
                             sm100::bulk_g2s(dst, static_cast<const uint8_t *>(a.k_pages) + at, TILE, full(st));
@@ -490,8 +531,6 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);
         }
-        if (lane == 0 && cur.end() >= hi) paged_join_of(a, cur, x, c, hi, total);
-        more = cur.end() < hi && cur.next(a);
     }
     if (!ok && lane == 0) a.joins[c].last = -1;
     // every copy must have landed before the block may end

@@ -52,11 +52,18 @@ __device__ __forceinline__ void mma8_f16(float (&c)[4], uint32_t a0, uint32_t a1
 }
 
 // A weight of 0 does not silence a NaN or an infinity.  So, where some row does not see all of
-// the 16 tokens whose V is in vf: tokens that no row sees (outside [kb, end)) are cleared, and
-// so is every value that is not finite; true (for the whole warp) if there was one, and then
-// add_left_out gives it to the rows that do see it.  key: that of the lane's first token.
+// the 16 tokens whose V is in vf, values that are not finite are taken out of vf, if there are any
+// (0 times a value, summed up, is NaN then): those of tokens that no row sees (outside
+// [kb, end)) for good, and true (for the whole warp) if others are left, which add_left_out then
+// gives to the rows that do see their token.  key: that of the lane's first token.
 template <typename T, int NV>
 __device__ __forceinline__ bool clear_unseen(uint32_t (&vf)[NV][2], int32_t key, int32_t kb, int32_t end) {
+    uint32_t test[2] = {0u, 0u};
+#pragma unroll
+    for (int n = 0; n < NV; ++n)
+#pragma unroll
+        for (int b = 0; b < 2; ++b) test[b] = Io<T>::add_zero_times(vf[n][b], test[b]);
+    if (!__any_sync(0xffffffffu, ((test[0] | test[1]) & 0x7fff7fffu) != 0u)) return false;
     bool odd = false;
 #pragma unroll
     for (int b = 0; b < 2; ++b) {

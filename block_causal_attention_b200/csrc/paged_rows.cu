@@ -113,6 +113,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     // j % 2, token group j / 2 of this warp; V: token group j % 2, channel group j / 2.
     const uint32_t kaddr = (lane >> 3 & 1) * (kPage * 16) + (2 * warp + (lane >> 4)) * 128 + (lane & 7) * 16;
     const uint32_t vaddr = ((2 * warp + (lane >> 3 & 1)) * D + 8 * (lane >> 4) + (lane & 7)) * 16;
+    float2 gain[Row8<D>::N];
+    Row8<D>::load_gain(a.pos ? a.q_gain : nullptr, lane & 7, gain);
     bool ok = true;
     int it = 0;
     for (int n_item = 0;; ++n_item) {
@@ -134,8 +136,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
             const int64_t row = x.row + x.token + (int32_t)(packed / a.group);
             Row8<D> q;
             q.load(static_cast<const T *>(a.q) + (row * a.hq + x.g * a.group + packed % a.group) * D,
-                   a.pos ? a.pos + row * 3 : nullptr, a.q_gain, e);
-            if (a.pos) q.prologue(a.turns, a.eps, e);
+                   a.pos ? a.pos + row * 3 : nullptr, e);
+            if (a.pos) q.prologue(gain, a.turns, a.eps, e);
 #pragma unroll
             for (int i = 0; i < Row8<D>::N; ++i)
                 if (e + 8 * i < D / 2)

@@ -41,19 +41,23 @@ struct TilesSmem {
     static constexpr int STAGES = D == 48 ? 6 : 8;
     static constexpr int Q_BYTES = 128 * DPAD * 2;
     static constexpr int OFF_Q = 0;
-    static constexpr int OFF_RING = kSlots * Q_BYTES;
+    static constexpr int Q_ITEM = kSlots * Q_BYTES;
+    static constexpr int OFF_RING = 2 * Q_ITEM;      // queries of this item and of the next
     static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE;
     static constexpr int B_FULL = 0;
     static constexpr int B_EMPTY = STAGES;
     static constexpr int B_ITEM = 2 * STAGES;
     static constexpr int B_S_FULL = B_ITEM + 2 * kItemRing;
     static constexpr int B_S_FREE = B_S_FULL + kSlots * kBuffers;  // full: of a slot's use of a buffer
-    static constexpr int B_Q = B_S_FREE + kBuffers;
-    static constexpr int B_DONE = B_Q + kSlots;
+    static constexpr int B_Q_FULL = B_S_FREE + kBuffers;
+    static constexpr int B_Q_FREE = B_Q_FULL + 2;
+    static constexpr int B_Q_FIRST = B_Q_FREE + 2;
+    static constexpr int B_DONE = B_Q_FIRST + 1;
     static constexpr int OFF_HERE = OFF_BAR + 8 * (B_DONE + 1);
     static constexpr int OFF_TMEM = OFF_HERE + 4 * STAGES;
     static constexpr int OFF_ITEMS = OFF_TMEM + 4;
-    static constexpr int OFF_ABORT = OFF_ITEMS + kItemRing * (int)sizeof(PagedItem);
+    static constexpr int OFF_LIMIT = OFF_ITEMS + kItemRing * (int)sizeof(PagedItem);  // of each row
+    static constexpr int OFF_ABORT = OFF_LIMIT + 4 * kRows;
     static constexpr int BYTES = OFF_ABORT + 4;
 };
 
@@ -73,6 +77,34 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&f)[4][4]) {
         : "r"(taddr));
 #pragma unroll
     for (int i = 0; i < 16; ++i) f[i / 4][i % 4] = __uint_as_float(r[i]);
+}
+
+// QK-Norm and RoPE of 16 packed rows of an item, from row `first` on, into the A operand of
+// S = Q K^T (fp16, K-major core matrices, tiles of 128 rows); a warp, eight lanes a row.
+template <int D, typename T>
+__device__ __forceinline__ void query_rows(const PagedArgs &a, const PagedItem &x, const float2 (&gain)[Row8<D>::N],
+                                           uint8_t *to, int first) {
+    const int e = threadIdx.x & 7, r0 = first + (threadIdx.x >> 3 & 3);
+    Row8<D> q[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t packed = x.head + min(r0 + 4 * i, x.left - 1);
+        const int64_t row = x.row + x.token + (int32_t)(packed / a.group);
+        q[i].load(static_cast<const T *>(a.q) + (row * a.hq + x.g * a.group + packed % a.group) * D,
+                  a.pos ? a.pos + row * 3 : nullptr, e);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int r = r0 + 4 * i;
+        if (a.pos) q[i].prologue(gain, a.turns, a.eps, e);
+#pragma unroll
+        for (int k = 0; k < Row8<D>::N; ++k) {
+            const int pr = e + 8 * k;
+            if (pr < D / 2)
+                *reinterpret_cast<uint32_t *>(to + r / 128 * TilesSmem<D>::Q_BYTES + (pr >> 2) * 2048 + r % 128 * 16 +
+                                              (pr & 3) * 4) = r < x.left ? pack_f16x2(q[i].x[k].x, q[i].x[k].y) : 0u;
+        }
+    }
 }
 
 template <int D, typename T>
@@ -103,18 +135,22 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
         }
         for (int i = 0; i < kSlots * kBuffers; ++i) mbar_init(bar(L::B_S_FULL + i), 1);
         for (int i = 0; i < kBuffers; ++i) mbar_init(bar(L::B_S_FREE + i), 4);
-        for (int s = 0; s < kSlots; ++s) mbar_init(bar(L::B_Q + s), 4);
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(bar(L::B_Q_FULL + i), 2);
+            mbar_init(bar(L::B_Q_FREE + i), 1);
+        }
         for (int i = 0; i < kItemRing; ++i) {
             mbar_init(bar(L::B_ITEM + i), 1);
-            mbar_init(bar(L::B_ITEM + kItemRing + i), 1 + 4 * kSlots);
+            mbar_init(bar(L::B_ITEM + kItemRing + i), 3 + 4 * kSlots);  // warps 1, 2, 3 and the softmax's
         }
+        mbar_init(bar(L::B_Q_FIRST), 4 * kSlots);
         mbar_init(bar(L::B_DONE), 1);
         mbar_fence_init();
     }
     if constexpr (L::DPAD > D) {
         // channels that do not exist: zero in Q and, so that 0 times them is 0, in every K stage
         constexpr int N = (L::KSTAGE - L::TILE) / 16;
-        for (int i = threadIdx.x; i < (S + kSlots) * N; i += kThreads) {
+        for (int i = threadIdx.x; i < (S + 2 * kSlots) * N; i += kThreads) {
             uint8_t *to = i / N < S ? smem + L::OFF_RING + i / N * L::STAGE + L::TILE
                                     : smem + L::OFF_Q + (i / N - S) * L::Q_BYTES + 128 * D * 2;
             reinterpret_cast<uint4 *>(to)[i % N] = make_uint4(0, 0, 0, 0);
@@ -140,8 +176,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
         // ------------------------------------------------ S = Q K^T
         if (lane == 0) {
             int it = 0;
-            int queries[kSlots] = {};  // query tiles of each slot so far
-            uint32_t made = 0;         // S tiles so far
+            uint32_t queries = 0;  // items with pages so far
+            uint32_t made = 0;     // S tiles so far
             bool ok = true;
             for (int n = 0; ok; ++n) {
                 ok = paged_wait(bar(L::B_ITEM + n % kItemRing), (n / kItemRing) & 1, a, abort_flag);
@@ -151,9 +187,11 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                 if (p0 < 0) break;
                 mbar_arrive(bar(L::B_ITEM + kItemRing + n % kItemRing));
                 if (p0 == p1) continue;
-#pragma unroll
-                for (int s = 0; s < kSlots; ++s)
-                    if (s * 128 < left) ok = ok && paged_wait(bar(L::B_Q + s), queries[s]++ & 1, a, abort_flag);
+                const uint32_t qb = queries % 2;
+                // (buffer 0 is first filled by the softmax warps, which have a barrier of their own)
+                ok = queries == 0 ? paged_wait(bar(L::B_Q_FIRST), 0, a, abort_flag)
+                                  : paged_wait(bar(L::B_Q_FULL + qb), (queries / 2 - (qb == 0)) & 1, a, abort_flag);
+                ++queries;
                 for (int32_t p = p0; p < p1 && ok; ++p, ++it) {
                     const int st = it % S;
                     ok = paged_wait(bar(L::B_FULL + st), (it / S) & 1, a, abort_flag);
@@ -166,7 +204,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                         if (!ok) continue;
                         ++made;
                         tc_fence_after();
-                        const uint32_t qa = sbase + L::OFF_Q + s * L::Q_BYTES;
+                        const uint32_t qa = sbase + L::OFF_Q + qb * L::Q_ITEM + s * L::Q_BYTES;
                         const uint32_t kb = sbase + L::OFF_RING + st * L::STAGE;
 #pragma unroll
                         for (int k = 0; k < L::DPAD / 16; ++k)
@@ -175,6 +213,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                         mma_commit(bar(L::B_S_FULL + s * kBuffers + buf));
                     }
                 }
+                mma_commit(bar(L::B_Q_FREE + qb));
             }
         }
         if (lane == 0) {
@@ -186,7 +225,41 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
             }
         }
         __syncwarp();
-    } else if (warp >= 4) {
+    } else if (warp < 4) {
+        // ------------------------------------------------ queries, an item ahead
+        // Two warps, 32 rows at a time, beside the softmax of the item before.  The block's first
+        // item has nothing to hide behind: all softmax warps make its queries.
+        const int e = lane & 7;
+        float2 gain[Row8<D>::N];
+        Row8<D>::load_gain(a.pos ? a.q_gain : nullptr, e, gain);
+        uint32_t queries = 0;
+        for (int n = 0;; ++n) {
+            if (!__all_sync(0xffffffffu,
+                            paged_wait(bar(L::B_ITEM + n % kItemRing), (n / kItemRing) & 1, a, abort_flag)))
+                break;
+            const PagedItem &x = items[n % kItemRing];
+            const int32_t p0 = x.p0, p1 = x.p1;
+            if (p0 < 0) break;
+            if (p0 < p1) {
+                const uint32_t qb = queries % 2;
+                if (queries >= 2 && !__all_sync(0xffffffffu, paged_wait(bar(L::B_Q_FREE + qb), (queries / 2 - 1) & 1, a,
+                                                                        abort_flag)))
+                    break;
+                ++queries;
+                if (queries > 1) {
+                    const int rows = min((x.left + 127) / 128 * 128, kRows);
+#pragma unroll 1
+                    for (int r = (warp - 2) * 16; r < rows; r += 32)
+                        query_rows<D, T>(a, x, gain, smem + L::OFF_Q + qb * L::Q_ITEM, r);
+                    fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(bar(L::B_Q_FULL + qb));
+                }
+            }
+            if (lane == 0) mbar_arrive(bar(L::B_ITEM + kItemRing + n % kItemRing));
+        }
+        __syncwarp();
+    } else {
         regs_inc<152>();
         // ------------------------------------------------ softmax and O += P V
         const int slot = (warp - 4) >> 2, quarter = warp & 3;
@@ -200,8 +273,10 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
         // buffers, so a barrier of a buffer alone would run through phases that this warp does not
         // wait for, and its parity would tell it nothing.
         uint32_t parity = 0;
+        bool first = true;
         bool ok = true;
         const int wr = slot * 128 + quarter * 32;  // the warp's first row of the work tile
+        int32_t *limits = reinterpret_cast<int32_t *>(smem + L::OFF_LIMIT) + wr;  // of this warp's rows
         for (int n_item = 0; ok; ++n_item) {
             const uint32_t done = bar(L::B_ITEM + kItemRing + n_item % kItemRing);
             ok = __all_sync(0xffffffffu, paged_wait(bar(L::B_ITEM + n_item % kItemRing), (n_item / kItemRing) & 1, a,
@@ -210,6 +285,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
             const PagedItem &x = items[n_item % kItemRing];
             const int32_t p0 = x.p0, p1 = x.p1;
             if (p0 < 0) break;
+            if (first && p0 < p1) {
+                first = false;
+                float2 gain[Row8<D>::N];
+                Row8<D>::load_gain(a.pos ? a.q_gain : nullptr, lane & 7, gain);
+#pragma unroll 1
+                for (int r = wr; r < wr + 32; r += 16) query_rows<D, T>(a, x, gain, smem + L::OFF_Q, r);
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(bar(L::B_Q_FIRST));
+            }
             const int active = (x.left + 127) / 128;  // slots that have rows
             if (slot * 128 >= x.left) {
                 for (int32_t p = p0; p < p1 && ok; ++p, ++it) {
@@ -232,33 +317,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                 ref[m][0] = ref[m][1] = -INFINITY;
                 sum[m][0] = sum[m][1] = 0.f;
             }
-            if (p0 < p1) {
-                // queries of this warp's 32 rows, as the A operand (K-major core matrices); the slot's
-                // last S is here, so the products that read the old ones are done
-#pragma unroll 2
-                for (int i = 0; i < 8; ++i) {
-                    const int r = quarter * 32 + i * 4 + (lane >> 3), e = lane & 7;
-                    const bool live = slot * 128 + r < x.left;
-                    const uint32_t packed = x.head + (live ? slot * 128 + r : 0);
-                    const int64_t row = x.row + x.token + (int32_t)(packed / a.group);
-                    Row8<D> q;
-                    q.load(static_cast<const T *>(a.q) + (row * a.hq + x.g * a.group + packed % a.group) * D,
-                   a.pos ? a.pos + row * 3 : nullptr, a.q_gain, e);
-                    if (a.pos) q.prologue(a.turns, a.eps, e);
-#pragma unroll
-                    for (int k = 0; k < Row8<D>::N; ++k) {
-                        const int pr = e + 8 * k;
-                        if (pr < D / 2)
-                            *reinterpret_cast<uint32_t *>(smem + L::OFF_Q + slot * L::Q_BYTES + (pr >> 2) * 2048 +
-                                                          r * 16 + (pr & 3) * 4) =
-                                live ? pack_f16x2(q.x[k].x, q.x[k].y) : 0u;
-                    }
-                }
-                fence_proxy_async_smem();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(bar(L::B_Q + slot));
-            }
             // keys that all, and that some of the warp's rows see end here
+            limits[lane] = x.limit(wr + lane, a.group);
+            __syncwarp();
             const int32_t lim_all = x.limit(min(wr, x.left - 1), a.group);
             const int32_t lim_any = x.limit(min(wr + 31, x.left - 1), a.group);
             const int32_t kb = x.kb;
@@ -435,14 +496,18 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
                             if (!inside) {
-                                const int32_t lim = x.limit(wr + 16 * m + 8 * h + g, a.group);
+                                const int32_t past = limits[16 * m + 8 * h + g] - key0 - 2 * t;
 #pragma unroll
                                 for (int n = 0; n < kTiles; ++n)
 #pragma unroll
-                                    for (int j = 0; j < 2; ++j) {
-                                        const int32_t key = key0 + 8 * n + 2 * t + j;
-                                        if (key < kb || key >= lim) s[m][n][2 * h + j] = -INFINITY;
-                                    }
+                                    for (int j = 0; j < 2; ++j)
+                                        if (8 * n + j >= past) s[m][n][2 * h + j] = -INFINITY;
+                                if (key0 < kb)
+#pragma unroll
+                                    for (int n = 0; n < kTiles; ++n)
+#pragma unroll
+                                        for (int j = 0; j < 2; ++j)
+                                            if (8 * n + j < kb - key0 - 2 * t) s[m][n][2 * h + j] = -INFINITY;
                             }
                             float top = s[m][0][2 * h];
 #pragma unroll
@@ -485,7 +550,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                             if (odd) {
                                 int32_t lim[2];
 #pragma unroll
-                                for (int h = 0; h < 2; ++h) lim[h] = x.limit(wr + 16 * m + 8 * h + g, a.group);
+                                for (int h = 0; h < 2; ++h) lim[h] = limits[16 * m + 8 * h + g];
                                 add_left_out<D, T, NV>(o[m], pa[m][k],
                                                        reinterpret_cast<const T *>(smem + (vs + at - sbase)), keyk, kb,
                                                        lim);
