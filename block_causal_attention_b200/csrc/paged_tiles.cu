@@ -478,7 +478,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                     }
                 }
                 const uint32_t vs = page_v(it % S);
-                // Else, or from the step on that passed kTop: with masks and the running maximum.
+                // Else, or from the step on that passed kTop: step by step, with masks and the running
+                // maximum where they are needed.
 #pragma unroll 1
                 for (; step < kSteps; ++step) {
                     const int32_t key0 = page0 + kChunk * step;
@@ -487,9 +488,19 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                         load_s(step);
                         wait_s();
                     }
+                    const bool inside = key0 >= kb && key0 + kChunk <= lim_all;
+                    if (work && inside && settled) {
+                        if (fast_step(false, 0, 0)) {
+                            if (step == kSteps - 1) free_s();
+                            products(vs, step, 0);
+                            products(vs, step, 1);
+                            continue;
+                        }
+                        load_s(step);
+                        wait_s();
+                    }
                     if (step == kSteps - 1) free_s();
                     if (!work) continue;
-                    const bool inside = key0 >= kb && key0 + kChunk <= lim_all;
                     settled = true;
 #pragma unroll
                     for (int m = 0; m < 2; ++m)
