@@ -290,6 +290,13 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     const PagedJoin j = a.joins[c];
     const int pieces = j.last - c + 1;
     if (j.last < c) return;
+    // The workspace is the caller's.  Two calls that overlap with one workspace may read each
+    // other's notes: their results are lost, but nothing outside their arrays is touched.
+    if (j.last >= a.shares || (uint32_t)j.g >= (uint32_t)a.hkv || (uint32_t)j.head >= (uint32_t)a.group ||
+        j.left > a.rows) {
+        if (threadIdx.x == 0) atomicOr(a.status, kPagedWorkspace);
+        return;
+    }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / 8, e = lane % 8;
     const size_t slot = (size_t)a.rows * (D + 2);
     const int rows = a.rows / gridDim.y;
@@ -342,8 +349,12 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         const bool none = ref == -INFINITY;
         const float inv = none ? 0.f : 1.f / sum;
         const uint32_t packed = j.head + row;
-        const int64_t token = j.row + j.token + (int32_t)(packed / a.group);
+        const int64_t token = (int64_t)j.row + j.token + (int32_t)(packed / a.group);
         const int head = j.g * a.group + (int)(packed % a.group);
+        if ((uint64_t)token >= (uint64_t)a.nq) {
+            if (e == 0) atomicOr(a.status, kPagedWorkspace);
+            continue;
+        }
         const int64_t at = (token * a.hq + head) * D;
 #pragma unroll
         for (int k = 0; k < D / 8; ++k) {
@@ -502,8 +513,8 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
     const double items = ((double)io.nq * a.group / a.rows + io.slices) * c.hkv;
     const double keys = std::max((double)io.width * kPage, (double)io.nq);
     a.shift = 0;
-    while (a.shift < 27 && items * (16.0 + std::ldexp(keys, -4 - a.shift)) > 2e9) ++a.shift;
-    if (items * 17.0 > 2e9) return BCA_ERR_TOO_LARGE;
+    while (a.shift < 27 && items * (64.0 + std::ldexp(keys, -4 - a.shift)) > 2e9) ++a.shift;
+    if (items * 65.0 > 2e9) return BCA_ERR_TOO_LARGE;
     const int rc = a.rows == kPagedTileRows ? launch_paged_tiles(c, a, stream) : launch_paged_rows(c, a, stream);
     if (rc != BCA_OK) return rc;
     return by_type(c, [&](auto d, auto t) { return launch_join<decltype(d)::value, decltype(t)>(a, stream); });

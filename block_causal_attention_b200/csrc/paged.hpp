@@ -18,6 +18,7 @@ constexpr int kPagedTileRows = 384;  // packed rows of a work item of paged_tile
 // status-word bits written by the paged kernels
 constexpr int kPagedTimeout = 0x1;
 constexpr int kPagedNoPage = 0x2;
+constexpr int kPagedWorkspace = 0x4;
 
 struct PagedCache {
     int hq = 0, hkv = 0, d = 0, layers = 1;

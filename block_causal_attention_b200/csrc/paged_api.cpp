@@ -184,7 +184,9 @@ int bca_paged_status(bca_paged_t cache, void *stream) {
     if (h == 0) return BCA_OK;
     if (cudaMemsetAsync(c.d_status, 0, sizeof(int), s) != cudaSuccess) return BCA_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return BCA_ERR_CUDA;
-    return (h & bca::kPagedTimeout) ? BCA_ERR_DEVICE_TIMEOUT : BCA_ERR_BAD_PAGE;
+    return (h & bca::kPagedTimeout)     ? BCA_ERR_DEVICE_TIMEOUT
+           : (h & bca::kPagedWorkspace) ? BCA_ERR_INVALID_ARGUMENT
+                                        : BCA_ERR_BAD_PAGE;
 }
 
 }  // extern "C"

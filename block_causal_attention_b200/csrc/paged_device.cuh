@@ -54,10 +54,16 @@ struct PagedArgs {
 // call gives the same bits.
 
 // Weight of an item that reads no page, in units of 16 << shift keys: its prologue, its epilogue
-// and the start of its loads, worth a page.  The whole row of items is below 2^31 units long
-// (the host picks the shift for the sizes of the call), so all of this is 32-bit arithmetic:
-// before a block knows what to load it can do nothing else, and 64-bit divisions here took 2 us.
-constexpr uint32_t kItemWeight = 8;
+// and its first page, as measured: one page of the register tiles, two pages of the 384-row
+// tiles, four with the causal rule, whose last pages are masked (fitted to the blocks' clocks:
+// 8,500 and 17,200 cycles an item beside 4,200 a page).  The whole row of items is below 2^31
+// units long (the host picks the shift for the sizes of the call), so all of this is 32-bit
+// arithmetic: before a block knows what to load it can do nothing else, and 64-bit divisions
+// here took 2 us.
+template <int R>
+__device__ __forceinline__ uint32_t paged_item_weight(bool causal) {
+    return R < kPagedTileRows ? 8u : causal ? 32u : 16u;
+}
 
 struct PagedSlice {
     int32_t r0, n;        // its rows of q
@@ -65,12 +71,15 @@ struct PagedSlice {
     int32_t kb, ke;       // keys [kb, ke) that it sees; kb == ke: none
     int32_t end;          // k_end as given (>= 0): the causal rule counts back from it
     uint32_t tiles;       // of one KV head
-    uint32_t w0, dw;      // weight of tile t: w0 + dw * (t + 1)
+    uint32_t w0, dw;      // weight of tile t: w0 + dw * (t + 1), and of the last one
+    uint32_t cut;         // this less: a 384-row tile with 128 or 256 rows takes less time
 
     __device__ __forceinline__ uint32_t upto(uint32_t t) const {  // weight of its first t tiles
-        return t * w0 + (dw == 0 ? 0u : dw * (t * (t + 1) / 2));
+        return t * w0 + (dw == 0 ? 0u : dw * (t * (t + 1) / 2)) - (t == tiles ? cut : 0u);
     }
-    __device__ __forceinline__ uint32_t weight(uint32_t t) const { return w0 + dw * (t + 1); }
+    __device__ __forceinline__ uint32_t weight(uint32_t t) const {
+        return w0 + dw * (t + 1) - (t + 1 == tiles ? cut : 0u);
+    }
 };
 
 template <int R>
@@ -78,7 +87,8 @@ __device__ __forceinline__ PagedSlice paged_slice(const PagedArgs &a, int i) {
     PagedSlice s;
     const int32_t nq = (int32_t)a.nq;
     const int32_t o0 = __ldg(a.off + i), o1 = __ldg(a.off + i + 1);
-    const int32_t b = a.seq ? __ldg(a.seq + i) : i, kb = __ldg(a.k_begin + i), ke = __ldg(a.k_end + i);
+    const int32_t row = __ldg((a.seq ? a.seq : a.off) + i), kb = __ldg(a.k_begin + i), ke = __ldg(a.k_end + i);
+    const int32_t b = a.seq ? row : i;
     s.r0 = min(max(o0, 0), nq);
     s.n = min(max(o1, s.r0), nq) - s.r0;
     s.b = b;
@@ -90,12 +100,19 @@ __device__ __forceinline__ PagedSlice paged_slice(const PagedArgs &a, int i) {
     s.tiles = ((uint32_t)s.n * (uint32_t)a.group + (R - 1)) / R;
     const int32_t keys = s.ke - s.kb;
     const int unit = 4 + a.shift;
+    const uint32_t item = paged_item_weight<R>(a.causal);
     if (a.causal) {
         s.dw = (uint32_t)R / (uint32_t)a.group >> unit;
-        s.w0 = kItemWeight + ((uint32_t)max(keys - s.n, 0) >> unit);
+        s.w0 = item + ((uint32_t)max(keys - s.n, 0) >> unit);
     } else {
         s.dw = 0;
-        s.w0 = kItemWeight + ((uint32_t)keys >> unit);
+        s.w0 = item + ((uint32_t)keys >> unit);
+    }
+    s.cut = 0;
+    if (R == kPagedTileRows && s.tiles > 0) {
+        // a page with one, two, three tiles of 128 rows: 0.55, 0.77, 1 of the time
+        const uint32_t slots = ((uint32_t)s.n * (uint32_t)a.group - (s.tiles - 1) * R + 127) / 128;
+        s.cut = (s.w0 + s.dw * s.tiles - item) * (3 - slots) / 4;
     }
     return s;
 }
@@ -218,6 +235,7 @@ __device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, uint32_t
     cur.s.tiles = give(s.tiles);
     cur.s.w0 = give(s.w0);
     cur.s.dw = give(s.dw);
+    cur.s.cut = give(s.cut);
     const uint32_t per_head = cur.s.upto(cur.s.tiles);
     uint32_t rest = lo - give(pre);
     cur.g = (int32_t)(rest / per_head);
@@ -386,23 +404,27 @@ struct Row8 {
     float2 x[N];
     int32_t at[N];
 
-    // The raw values and the positions, on the way at the same time.
+    // The raw values and the positions, on the way at the same time.  pos: any three words that
+    // may be read where there are no positions.
     template <typename T>
     __device__ __forceinline__ void load(const T *row, const int32_t *pos, int e) {
 #pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int p = e + 8 * i;
-            x[i] = p < D / 2 ? Io<T>::unpack(__ldg(reinterpret_cast<const uint32_t *>(row) + p)) : float2{0.f, 0.f};
-            at[i] = pos && p < 3 * P ? __ldg(pos + p / P) : 0;
+            const int p = min(e + 8 * i, D / 2 - 1);  // lanes without a pair read the last one again
+            x[i] = Io<T>::unpack(__ldg(reinterpret_cast<const uint32_t *>(row) + p));
+            if (e + 8 * i >= D / 2) x[i] = make_float2(0.f, 0.f);
+            at[i] = __ldg(pos + min(p / P, 2));
         }
     }
     // The lane's part of the QK-Norm gain.
     static __device__ __forceinline__ void load_gain(const float *gain, int e, float2 (&gn)[N]) {
 #pragma unroll
+        for (int i = 0; i < N; ++i) gn[i] = make_float2(1.f, 1.f);
+        if (gain == nullptr) return;
+#pragma unroll
         for (int i = 0; i < N; ++i) {
-            const int p = e + 8 * i;
-            gn[i] = gain && p < D / 2 ? make_float2(__ldg(gain + 2 * p), __ldg(gain + 2 * p + 1))
-                                      : make_float2(1.f, 1.f);
+            const int p = min(e + 8 * i, D / 2 - 1);
+            gn[i] = make_float2(__ldg(gain + 2 * p), __ldg(gain + 2 * p + 1));
         }
     }
     // QK-Norm and RoPE.

@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     const uint32_t kaddr = (lane >> 3 & 1) * (kPage * 16) + (2 * warp + (lane >> 4)) * 128 + (lane & 7) * 16;
     const uint32_t vaddr = ((2 * warp + (lane >> 3 & 1)) * D + 8 * (lane >> 4) + (lane & 7)) * 16;
     float2 gain[Row8<D>::N];
-    Row8<D>::load_gain(a.pos ? a.q_gain : nullptr, lane & 7, gain);
+    Row8<D>::load_gain(a.q_gain, lane & 7, gain);
     bool ok = true;
     int it = 0;
     for (int n_item = 0;; ++n_item) {
@@ -136,7 +136,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
             const int64_t row = x.row + x.token + (int32_t)(packed / a.group);
             Row8<D> q;
             q.load(static_cast<const T *>(a.q) + (row * a.hq + x.g * a.group + packed % a.group) * D,
-                   a.pos ? a.pos + row * 3 : nullptr, e);
+                   a.pos ? a.pos + row * 3 : static_cast<const int32_t *>(a.q), e);
             if (a.pos) q.prologue(gain, a.turns, a.eps, e);
 #pragma unroll
             for (int i = 0; i < Row8<D>::N; ++i)

@@ -91,7 +91,7 @@ __device__ __forceinline__ void query_rows(const PagedArgs &a, const PagedItem &
         const uint32_t packed = x.head + min(r0 + 4 * i, x.left - 1);
         const int64_t row = x.row + x.token + (int32_t)(packed / a.group);
         q[i].load(static_cast<const T *>(a.q) + (row * a.hq + x.g * a.group + packed % a.group) * D,
-                  a.pos ? a.pos + row * 3 : nullptr, e);
+                  a.pos ? a.pos + row * 3 : static_cast<const int32_t *>(a.q), e);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
@@ -174,9 +174,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                                                     bar(L::B_ITEM), items, here, abort_flag);
     } else if (warp == 1) {
         // ------------------------------------------------ S = Q K^T
+        uint32_t queries = 0;  // items with pages so far
         if (lane == 0) {
             int it = 0;
-            uint32_t queries = 0;  // items with pages so far
             uint32_t made = 0;     // S tiles so far
             bool ok = true;
             for (int n = 0; ok; ++n) {
@@ -217,9 +217,15 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
             }
         }
         if (lane == 0) {
-            // all issued products must be complete before the tensor memory is given back
+            // all issued products must be complete before the tensor memory is given back, and all
+            // arrivals made before the barriers' memory is
             mma_commit(bar(L::B_DONE));
-            if (!mbar_wait(bar(L::B_DONE), 0, a.timeout_ns)) {
+            bool done = mbar_wait(bar(L::B_DONE), 0, a.timeout_ns);
+            for (uint32_t b = 0; b < 2; ++b) {
+                const uint32_t uses = (queries + 1 - b) / 2;
+                if (uses > 0) done = done && mbar_wait(bar(L::B_Q_FREE + b), (uses - 1) & 1, a.timeout_ns);
+            }
+            if (!done) {
                 atomicOr(a.status, kPagedTimeout);
                 *abort_flag = 1;
             }
@@ -231,7 +237,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
         // item has nothing to hide behind: all softmax warps make its queries.
         const int e = lane & 7;
         float2 gain[Row8<D>::N];
-        Row8<D>::load_gain(a.pos ? a.q_gain : nullptr, e, gain);
+        Row8<D>::load_gain(a.q_gain, e, gain);
         uint32_t queries = 0;
         for (int n = 0;; ++n) {
             if (!__all_sync(0xffffffffu,
@@ -256,6 +262,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
                     if (lane == 0) mbar_arrive(bar(L::B_Q_FULL + qb));
                 }
             }
+            __syncwarp();
             if (lane == 0) mbar_arrive(bar(L::B_ITEM + kItemRing + n % kItemRing));
         }
         __syncwarp();
@@ -288,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
             if (first && p0 < p1) {
                 first = false;
                 float2 gain[Row8<D>::N];
-                Row8<D>::load_gain(a.pos ? a.q_gain : nullptr, lane & 7, gain);
+                Row8<D>::load_gain(a.q_gain, lane & 7, gain);
 #pragma unroll 1
                 for (int r = wr; r < wr + 32; r += 16) query_rows<D, T>(a, x, gain, smem + L::OFF_Q, r);
                 fence_proxy_async_smem();

@@ -151,7 +151,8 @@ class PagedCache:
             return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def status(self, stream=None) -> int:
-        """Status of the work on `stream`, waited for: BCA_OK, BCA_ERR_DEVICE_TIMEOUT, or
+        """Status of the work on `stream`, waited for: BCA_OK, BCA_ERR_DEVICE_TIMEOUT,
+        BCA_ERR_INVALID_ARGUMENT when overlapping calls shared a workspace and noticed it, or
         BCA_ERR_BAD_PAGE when a written token had no page.  Reading it clears it."""
         if stream is None and not self.host_only:
             stream = torch.cuda.current_stream(self.device)
