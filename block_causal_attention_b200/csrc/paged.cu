@@ -279,12 +279,14 @@ int launch_copy(const CopyArgs &a, const PagedCache &c, const int32_t *pairs, in
 // pieces p of an item, always in the order of the blocks that made them.  Block c joins the
 // item that share c begins and does not end.  A warp takes a row: first its pieces' references
 // and sums, a lane each, then O, eight lanes a piece, with the loads of 32 pieces on the way
-// at a time: three trips to memory whatever their number up to 32.
+// at a time: three trips to memory whatever their number up to 32, and two, four rows a warp,
+// for up to four.
 
 constexpr int kJoinThreads = 256;
+constexpr int kJoinFew = 4;  // pieces that are joined in one go
 
 template <int D, typename T>
-__global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_constant__ PagedArgs a) {
+__global__ void __launch_bounds__(kJoinThreads, 3) paged_join_kernel(const __grid_constant__ PagedArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const int c = blockIdx.x;
     const PagedJoin j = a.joins[c];
@@ -299,8 +301,59 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
     }
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, sub = lane / 8, e = lane % 8;
     const size_t slot = (size_t)a.rows * (D + 2);
-    const int rows = a.rows / gridDim.y;
-    for (int row = blockIdx.y * rows + warp; row < min((int)(blockIdx.y + 1) * rows, j.left); row += kJoinThreads / 32) {
+    const int rows = a.rows / gridDim.y, row_end = min((int)(blockIdx.y + 1) * rows, j.left);
+    // O / l and the LSE of a row, eight lanes
+    auto write = [&](int row, float ref, float sum, const float (&o)[D / 8]) {
+        const bool none = ref == -INFINITY;
+        const float inv = none ? 0.f : 1.f / sum;
+        const uint32_t packed = j.head + row;
+        const int64_t token = (int64_t)j.row + j.token + (int32_t)(packed / a.group);
+        const int head = j.g * a.group + (int)(packed % a.group);
+        if ((uint64_t)token >= (uint64_t)a.nq) {
+            if (e == 0) atomicOr(a.status, kPagedWorkspace);
+            return;
+        }
+        const int64_t at = (token * a.hq + head) * D;
+#pragma unroll
+        for (int k = 0; k < D / 8; ++k) {
+            const float y = none ? 0.f : o[k] * inv;
+            if (a.o_fp32) static_cast<float *>(a.o)[at + e + 8 * k] = y;
+            else static_cast<T *>(a.o)[at + e + 8 * k] = T(y);
+        }
+        if (a.lse && e == 0)
+            a.lse[head * a.nq + token] = none ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+    };
+
+    if (pieces <= kJoinFew) {
+        // few pieces, as the 384-row tiles have: four rows a warp, everything of a row on the way at once
+        for (int row = blockIdx.y * rows + 4 * warp + sub; row < row_end; row += kJoinThreads / 8) {
+            float r[kJoinFew], l[kJoinFew], y[kJoinFew][D / 8];
+#pragma unroll
+            for (int x = 0; x < kJoinFew; ++x) {
+                const float *part = a.part + (2 * (size_t)(c + x) + (x == 0 ? 1 : 0)) * slot;
+                const bool on = x < pieces;
+                r[x] = on ? part[(size_t)a.rows * D + row] : -INFINITY;
+                l[x] = on ? part[(size_t)a.rows * (D + 1) + row] : 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) y[x][k] = on ? part[(size_t)row * D + e + 8 * k] : 0.f;
+            }
+            float top = r[0], sum = 0.f, o[D / 8] = {};
+#pragma unroll
+            for (int x = 1; x < kJoinFew; ++x) top = fmaxf(top, r[x]);
+#pragma unroll
+            for (int x = 0; x < kJoinFew; ++x) {
+                if (r[x] == -INFINITY) continue;  // a piece without keys: it has no O, and may have no sum
+                const float w = sm100::ex2(r[x] - top);
+                sum = fmaf(l[x], w, sum);
+#pragma unroll
+                for (int k = 0; k < D / 8; ++k) o[k] = fmaf(y[x][k], w, o[k]);
+            }
+            write(row, top, sum, o);
+        }
+        return;
+    }
+
+    for (int row = blockIdx.y * rows + warp; row < row_end; row += kJoinThreads / 32) {
         float ref = -INFINITY, sum = 0.f, o[D / 8] = {};
         for (int base = 0; base < pieces; base += 32) {
             const int x = base + lane;
@@ -345,25 +398,8 @@ __global__ void __launch_bounds__(kJoinThreads) paged_join_kernel(const __grid_c
         for (int s = 8; s < 32; s <<= 1)
 #pragma unroll
             for (int k = 0; k < D / 8; ++k) o[k] += __shfl_xor_sync(0xffffffffu, o[k], s);
-        if (sub != 0) continue;
-        const bool none = ref == -INFINITY;
-        const float inv = none ? 0.f : 1.f / sum;
-        const uint32_t packed = j.head + row;
-        const int64_t token = (int64_t)j.row + j.token + (int32_t)(packed / a.group);
-        const int head = j.g * a.group + (int)(packed % a.group);
-        if ((uint64_t)token >= (uint64_t)a.nq) {
-            if (e == 0) atomicOr(a.status, kPagedWorkspace);
-            continue;
-        }
-        const int64_t at = (token * a.hq + head) * D;
-#pragma unroll
-        for (int k = 0; k < D / 8; ++k) {
-            const float y = none ? 0.f : o[k] * inv;
-            if (a.o_fp32) static_cast<float *>(a.o)[at + e + 8 * k] = y;
-            else static_cast<T *>(a.o)[at + e + 8 * k] = T(y);
-        }
-        if (a.lse && e == 0)
-            a.lse[head * a.nq + token] = none ? -INFINITY : (ref + log2f(sum)) * 0.69314718055994531f;
+        if (sub == 0) write(row, ref, sum, o);
+        __syncwarp();
     }
 }
 
