@@ -5,7 +5,7 @@
 // one pass over the keys: the reference r_i follows the running maximum.
 //
 // Bound by memory: a key and value of a KV head are 4 D bytes for 4 D * rows operations, so at
-// 16 to 64 rows even the warps' own matrix instructions keep up.  What counts is bytes in
+// 16 or 32 rows even the warps' own matrix instructions keep up.  What counts is bytes in
 // flight: one block a multiprocessor, a ring of whole pages (a page's keys and values of one
 // head are two contiguous stretches, moved by two bulk copies) filled by one warp that runs
 // ahead over page and item borders.  Eight warps take 16 of a page's 128 tokens each; their
@@ -38,7 +38,7 @@ struct RowsSmem {
     static constexpr int QSTRIDE = D == 24 ? 40 : D + 8;  // elements; an odd number of 16-byte units
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_Q = STAGES * 2 * TILE;
-    static constexpr int OFF_MERGE = OFF_Q + 64 * QSTRIDE * 2;
+    static constexpr int OFF_MERGE = OFF_Q + 32 * QSTRIDE * 2;
     static constexpr int OFF_BAR = OFF_MERGE + kWarps * 16 * (D + 2) * 4;
     static constexpr int OFF_HERE = OFF_BAR + 2 * (STAGES + kItemRing) * 8;
     static constexpr int OFF_ITEMS = OFF_HERE + STAGES * 4;
@@ -332,11 +332,7 @@ ldsm_v<NV>(vs + vaddr, vf);
 
 template <int D, typename T>
 const void *rows_kernel(int rows) {
-    switch (rows) {
-        case 16: return (const void *)paged_rows_kernel<D, T, 1>;
-        case 32: return (const void *)paged_rows_kernel<D, T, 2>;
-        default: return (const void *)paged_rows_kernel<D, T, 4>;
-    }
+    return rows == 16 ? (const void *)paged_rows_kernel<D, T, 1> : (const void *)paged_rows_kernel<D, T, 2>;
 }
 
 const void *rows_kernel(const PagedCache &c, int rows, int &bytes) {
@@ -357,7 +353,7 @@ const void *rows_kernel(const PagedCache &c, int rows, int &bytes) {
 }  // namespace
 
 int prepare_paged_rows(const PagedCache &c) {
-    for (int rows : {16, 32, 64}) {
+    for (int rows : {16, 32}) {
         int bytes = 0;
         const void *f = rows_kernel(c, rows, bytes);
         if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
