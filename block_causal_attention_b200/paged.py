@@ -221,8 +221,8 @@ class PagePool:
         return page
 
     def grow(self, seq: int, begin: int, end: int) -> List[tuple]:
-        """Make tokens [begin, end) of the sequence writable: pages up to `end` exist (released
-        ones in that stretch come back, empty), and those that [begin, end) touches are its
+        """Make tokens [begin, end) of the sequence writable: the pages that they touch exist
+        (released ones come back, empty; pages skipped before `begin` stay absent) and are its
         own.  Returns the page copies to make before the write.  Raises MemoryError, with
         nothing changed, when the pool has too few free pages."""
         if begin < 0 or end < begin:
@@ -232,7 +232,7 @@ class PagePool:
             return []
         first, last = begin // PAGE, (end + PAGE - 1) // PAGE
         touched = range(first, min(last, len(row)))
-        need = max(0, last - len(row)) + sum(1 for i in touched if row[i] < 0 or self._users[row[i]] > 1)
+        need = max(0, last - max(first, len(row))) + sum(1 for i in touched if row[i] < 0 or self._users[row[i]] > 1)
         if need > len(self._free):
             raise MemoryError(f"{need} pages needed, {len(self._free)} free")
         moves = []
@@ -246,7 +246,7 @@ class PagePool:
                 if i * PAGE < begin or (i + 1) * PAGE > end:   # else every slot is written anew
                     moves.append((old, row[i]))
         while len(row) < last:
-            row.append(self._take())
+            row.append(self._take() if len(row) >= first else -1)
         return moves
 
     def fork(self, seq: int) -> int:

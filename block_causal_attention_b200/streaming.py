@@ -24,11 +24,16 @@ Readings taken here (the pages give the idea, not the indexing):
 The slice list of a step depends only on the ranges of the W window positions, so plans are
 compiled once per distinct range tuple and reused: each step only moves the plan's start
 frame (``Plan.update_positions``), which rewrites the RoPE tables and nothing else.
+
+Two forms: ``PipelinedWindow`` drives plans over a contiguous cache of one video; ``PagedWindow``
+drives any number of videos, each at its own chunk, over one paged cache, where keys and values
+are written once and stay, and a video can be forked.
 """
 from __future__ import annotations
 
 import time
-from typing import Dict, Iterable, Optional, Sequence, Tuple
+from dataclasses import dataclass
+from typing import Any, Dict, Iterable, List, Optional, Sequence, Tuple
 
 import numpy as np
 
@@ -107,3 +112,168 @@ class PipelinedWindow:
         for p in self._plans.values():
             p.close()
         self._plans.clear()
+
+
+@dataclass
+class PagedStep:
+    """What the layers of one step of a ``PagedWindow`` share: which videos, where their tokens
+    go and what they see (int32 tensors on the cache's device)."""
+    videos: Tuple[int, ...]
+    rows: int                # tokens of all windows
+    table: Any               # [videos, width]
+    row_off: Any             # [videos + 1] rows of each video
+    start: Any               # [videos] first token of each window in its table row
+    slice_off: Any           # [videos * window + 1] rows of each chunk
+    seq: Any
+    k_begin: Any
+    k_end: Any
+    pos: Any                 # [rows, 3]
+
+
+class PagedWindow:
+    """The denoising windows of several videos over one paged KV cache.
+
+    Every video has the same geometry and its own window position (``open(first_chunk)``,
+    ``slide``), KV-range transitions and pages.  A step: ``begin(videos)`` once, then ``run`` for
+    each layer with the windows' tokens of all those videos, row after row.  The keys and values
+    of a window chunk are written anew each step; the last ones, from the step before the chunk
+    leaves the window, are what later chunks read.  ``fork`` continues a video in two ways: the
+    pages are shared until one of the two writes to them."""
+
+    def __init__(self, hq: int, hkv: int, d: int, frames: int, height: int, width: int, window: int,
+                 cache_chunks: int, kv_range: int, videos: int, layers: int = 1, rope_base=(1e4, 1e4, 1e4),
+                 eps: float = 1e-6, dtype=None, o_fp32: bool = False, pages: Optional[int] = None,
+                 host_only: bool = False):
+        """videos: how many are open at most; pages: the pool's size (default: enough for that
+        many windows with their caches, nothing shared)."""
+        from .paged import PAGE, PagedCache, PagePool
+        self._page = PAGE
+        self._schedule = lambda: PipelinedWindow(hq, hkv, d, frames, height, width, window, cache_chunks, kv_range,
+                                                 rope_base, eps, o_fp32, host_only=True)
+        geometry = self._schedule()
+        self.frames, self.height, self.width, self.window = frames, height, width, window
+        self.cache_chunks, self.chunk_tokens = cache_chunks, geometry.chunk_tokens
+        span = (cache_chunks + window + 1) * self.chunk_tokens   # while a window slides, one chunk more
+        pages = videos * (-(-span // PAGE) + 1) if pages is None else pages
+        self.cache = PagedCache(hq, hkv, d, pages, layers=layers, dtype=dtype, rope_base=rope_base, eps=eps,
+                                o_fp32=o_fp32, host_only=host_only)
+        self.pool = PagePool(pages)
+        self._videos: Dict[int, PipelinedWindow] = {}
+        self._first: Dict[int, int] = {}
+        self._oldest: Dict[int, int] = {}    # the first chunk that was ever in the window
+        self.pending_copies: List[Tuple[int, int]] = []   # that the tables count on already
+
+    # ------------------------------------------------------------------ videos
+    def open(self, first_chunk: int = 0) -> int:
+        """A new video whose window starts at absolute chunk `first_chunk`.  Chunks before that
+        one were never written: no range reaches them."""
+        if first_chunk < 0:
+            raise ValueError("first_chunk >= 0 is required")
+        video = self.pool.open()
+        self._videos[video], self._first[video] = self._schedule(), first_chunk
+        self._oldest[video] = first_chunk
+        return video
+
+    def _get(self, video: int) -> PipelinedWindow:
+        if video not in self._videos:
+            raise KeyError(f"no open video {video}")
+        return self._videos[video]
+
+    def first_chunk(self, video: int) -> int:
+        self._get(video)
+        return self._first[video]
+
+    def add_transition(self, video: int, chunk: int, stages: Iterable[int], kv_range: int = 1) -> None:
+        self._get(video).add_transition(chunk, stages, kv_range)
+
+    def slide(self, video: int) -> None:
+        """The window moves on by one chunk; pages that no window chunk can see any more go back."""
+        self._get(video)
+        self._first[video] += 1
+        self.pool.release_before(video, (self._first[video] - self.cache_chunks) * self.chunk_tokens)
+
+    def fork(self, video: int) -> int:
+        old = self._get(video)
+        new = self.pool.fork(video)
+        self._videos[new], self._first[new] = self._schedule(), self._first[video]
+        self._oldest[new] = self._oldest[video]
+        self._videos[new].transitions.update(old.transitions)
+        return new
+
+    def close_video(self, video: int) -> None:
+        self._get(video)
+        self.pool.close(video)
+        del self._videos[video], self._first[video], self._oldest[video]
+
+    def compact(self, stream=None) -> int:
+        """Move the pages in use to the front of the pool; returns how many moved.  Steps begun
+        before hold old tables: begin them again."""
+        self._copy_pending(stream)
+        self.pending_copies = self.pool.compact()
+        return self._copy_pending(stream)
+
+    def _copy_pending(self, stream) -> int:
+        n = len(self.pending_copies)
+        if n:
+            self.cache.copy_pages(self.pending_copies, stream=stream)
+            self.pending_copies = []
+        return n
+
+    # ------------------------------------------------------------------ steps
+    def layout(self, videos: Sequence[int]):
+        """The host side of ``begin``: (table, first token of each window in its row, (table row,
+        begin, end) of the keys of each window chunk).  Copies of shared pages that have to be made
+        first are added to ``pending_copies`` (also when the pool runs out half way)."""
+        if len(set(videos)) != len(videos):
+            raise ValueError("a video can be in a step once")
+        C, starts, seen, bases = self.chunk_tokens, [], [], []
+        for v in videos:   # all checked before any page is taken
+            self._get(v)
+        for b, v in enumerate(videos):
+            first = self._first[v]
+            self.pending_copies += self.pool.grow(v, first * C, (first + self.window) * C)
+            oldest = self._oldest[v]
+            base = max(oldest, first - self.cache_chunks) * C // self._page * self._page   # the row's first page
+            bases.append(base // self._page)
+            starts.append(first * C - base)
+            for p, r in enumerate(self._videos[v].ranges(first)):
+                seen.append((b, (first + p - min(r, first + p - oldest)) * C - base, (first + p + 1) * C - base))
+        rows = [self.pool.row(v)[skip:] for v, skip in zip(videos, bases)]
+        table = np.full((len(rows), max((len(r) for r in rows), default=0)), -1, np.int32)
+        for b, r in enumerate(rows):
+            table[b, :len(r)] = r
+        return table, starts, seen
+
+    def begin(self, videos: Sequence[int], stream=None) -> PagedStep:
+        """Pages for the windows of `videos` (copied first where they are shared) and the step's
+        device data."""
+        import torch
+        self._copy_pending(stream)   # of a step that found no page: before new ones can build on them
+        table, starts, seen = self.layout(videos)
+        with torch.cuda.stream(stream):
+            self._copy_pending(stream)
+            dev, C, per = self.cache.device, self.chunk_tokens, self.window * self.chunk_tokens
+            n, i32 = len(videos) * per, torch.int32
+            small = torch.tensor(starts + [x for row in seen for x in row], dtype=i32).to(dev)
+            keys = small[len(starts):].view(-1, 3).t().contiguous()
+            t = torch.arange(per, dtype=i32, device=dev)
+            plane = self.height * self.width
+            pos = torch.stack([t // plane, t % plane // self.width, t % self.width], 1).repeat(len(videos), 1)
+            begun = torch.tensor([self._first[v] * self.frames for v in videos], dtype=i32).to(dev)
+            pos[:, 0] += begun.repeat_interleave(per)
+            return PagedStep(tuple(videos), n, torch.from_numpy(table).to(dev),
+                             torch.arange(0, n + 1, per, dtype=i32, device=dev), small[:len(starts)],
+                             torch.arange(0, n + 1, C, dtype=i32, device=dev), keys[0], keys[1], keys[2], pos)
+
+    def run(self, step: PagedStep, q, k, v, *, layer: int = 0, q_gain=None, k_gain=None, o=None, lse=None,
+            stream=None):
+        """Write k, v [rows, Hkv, D] of the step's windows and attend q [rows, Hq, D]; returns o."""
+        if k.shape[0] != step.rows or q.shape[0] != step.rows:
+            raise ValueError(f"expected {step.rows} rows of q, k and v")
+        self.cache.write(k, v, step.table, step.row_off, step.start, pos=step.pos, k_gain=k_gain, layer=layer,
+                         stream=stream)
+        return self.cache.attend(q, step.table, step.slice_off, step.k_begin, step.k_end, seq=step.seq, pos=step.pos,
+                                 q_gain=q_gain, layer=layer, o=o, lse=lse, stream=stream)
+
+    def close(self) -> None:
+        self.cache.close()

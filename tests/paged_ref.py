@@ -80,6 +80,14 @@ def attend(q, k_pages, v_pages, table, off, seq, k_begin, k_end, causal, pos=Non
     return o, lse, bo, bl
 
 
+def attend_rows(q, k_pages, v_pages, table, off, seq, k_begin, k_end, rows, pos=None, gain=None):
+    """``attend`` of some rows of full slices: (O [rows], LSE [Hq, rows], and their bounds)."""
+    which = [max(i for i in range(len(seq)) if off[i] <= r) for r in rows]
+    return attend(q[rows], k_pages, v_pages, table, list(range(len(rows) + 1)), [seq[i] for i in which],
+                  [k_begin[i] for i in which], [k_end[i] for i in which], False,
+                  None if pos is None else pos[rows], gain)
+
+
 def pools(pages, hkv, d, dtype, gen, layers=1):
     k = torch.empty((layers, pages, hkv, d // 8, PAGE, 8), dtype=torch.float16, device="cuda").normal_(generator=gen)
     v = torch.empty((layers, pages, hkv, PAGE // 8, d, 8), dtype=dtype, device="cuda").normal_(generator=gen)

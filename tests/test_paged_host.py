@@ -185,3 +185,15 @@ def test_page_pool_tables_and_refusals():
     with pytest.raises(ValueError):
         PagePool(0)
     assert p.grow(b, 256, 384) == [] and p.free_pages == 1
+
+
+def test_pages_skipped_before_the_first_token_stay_absent():
+    p = PagePool(3)
+    a = p.open()
+    assert p.grow(a, 5 * PAGE + 100, 7 * PAGE) == [] and p.row(a) == [-1] * 5 + [0, 1] and p.free_pages == 1
+    assert p.grow(a, 3 * PAGE, 3 * PAGE + 1) == [] and p.row(a) == [-1] * 3 + [2, -1, 0, 1]
+    with pytest.raises(MemoryError):
+        p.grow(a, 9 * PAGE, 9 * PAGE + 1)
+    assert len(p.row(a)) == 7
+    p.close(a)
+    assert p.free_pages == 3
