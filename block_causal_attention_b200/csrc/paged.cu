@@ -294,7 +294,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) paged_join_kernel(const __gri
     if (j.last < c) return;
     // The workspace is the caller's.  Two calls that overlap with one workspace may read each
     // other's notes: their results are lost, but nothing outside their arrays is touched.
-    if (j.last >= a.shares || (uint32_t)j.g >= (uint32_t)a.hkv || (uint32_t)j.head >= (uint32_t)a.group ||
+    if (j.last >= kPagedShares || (uint32_t)j.g >= (uint32_t)a.hkv || (uint32_t)j.head >= (uint32_t)a.group ||
         j.left > a.rows) {
         if (threadIdx.x == 0) atomicOr(a.status, kPagedWorkspace);
         return;
@@ -406,7 +406,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) paged_join_kernel(const __gri
 template <int D, typename T>
 int launch_join(const PagedArgs &a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)a.shares, (unsigned)(a.rows < kPagedTileRows ? a.rows / 8 : 12));
+    cfg.gridDim = dim3((unsigned)kPagedShares, (unsigned)(a.rows < kPagedTileRows ? a.rows / 8 : 12));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};
@@ -438,17 +438,14 @@ int by_type(const PagedCache &c, F &&f) {
 //   16-row tiles        33 / 40     57 / 67    106 / 118   203 / 220   397 / 431
 //   32-row tiles        47 / 54     48 / 55     86 / 97    164 / 182   316 / 350
 //   384-row tiles       89 / 111    90 / 112    91 / 114    92 / 116   123 / 155
-PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices) {
-    PagedShape s;
+int paged_tile_rows(const PagedCache &c, int64_t nq, int slices) {
     const int64_t rows = nq * (c.hq / c.hkv) / std::max(slices, 1);
-    s.rows = rows <= 16 ? 16 : rows <= 64 ? 32 : kPagedTileRows;
-    s.shares = kSMs;
-    return s;
+    return rows <= 16 ? 16 : rows <= 64 ? 32 : kPagedTileRows;
 }
 
 size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices) {
-    const PagedShape s = paged_shape(c, nq, slices);
-    return (size_t)s.shares * (kPagedJoinBytes + 2 * s.rows * (c.d + 2) * sizeof(float));
+    const size_t rows = (size_t)paged_tile_rows(c, nq, slices);
+    return kPagedShares * (kPagedJoinBytes + 2 * rows * (c.d + 2) * sizeof(float));
 }
 
 int prepare_paged(const PagedCache &c) {
@@ -516,7 +513,6 @@ int launch_paged_copy(const PagedCache &c, const int32_t *pairs, int64_t n, void
 }
 
 int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream_t stream) {
-    const PagedShape s = paged_shape(c, io.nq, io.slices);
     PagedArgs a;
     a.q = io.q;
     a.pos = io.pos;
@@ -531,7 +527,7 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
     a.o = io.o;
     a.lse = io.lse;
     a.joins = static_cast<PagedJoin *>(io.workspace);
-    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(io.workspace) + (size_t)s.shares * kPagedJoinBytes);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(io.workspace) + (size_t)kPagedShares * kPagedJoinBytes);
     a.status = c.d_status;
     a.nq = io.nq;
     a.pages = c.pages;
@@ -542,8 +538,7 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
     a.hq = c.hq;
     a.hkv = c.hkv;
     a.group = c.hq / c.hkv;
-    a.rows = s.rows;
-    a.shares = s.shares;
+    a.rows = paged_tile_rows(c, io.nq, io.slices);
     a.o_fp32 = (c.flags & BCA_O_FP32) ? 1 : 0;
     a.eps = c.eps;
     a.scale = 1.4426950408889634f / std::sqrt((float)c.d);

@@ -11,7 +11,7 @@
 namespace bca {
 
 constexpr int kPage = BCA_PAGE_TOKENS;
-constexpr int kSMs = 148;
+constexpr int kPagedShares = 148;    // blocks of an attention call: one a multiprocessor
 constexpr int kPagedJoinBytes = 32;  // of the workspace, for each share
 constexpr int kPagedTileRows = 384;  // packed rows of a work item of paged_tiles.cu
 
@@ -59,15 +59,9 @@ struct PagedAttendIO {
     void *workspace;
 };
 
-// How a call's work is cut: tiles of `rows` packed (token, head of the KV group) rows, the
-// whole of it in `shares` equal stretches, a block each.
-struct PagedShape {
-    int rows;
-    int shares;
-};
-
-// The cut of a call of these sizes (the same for the workspace and the launch).
-PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices);
+// Packed (token, head of the KV group) rows of the tiles that a call of these sizes is cut into
+// (the same for the workspace and the launch).
+int paged_tile_rows(const PagedCache &c, int64_t nq, int slices);
 size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices);
 
 int prepare_paged(const PagedCache &c);

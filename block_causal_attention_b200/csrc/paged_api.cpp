@@ -103,8 +103,8 @@ int bca_paged_write(bca_paged_t cache, const void *k, const void *v, int64_t n, 
     const PagedCache &c = cache->cache;
     int rc = on_its_device(c);
     if (rc != BCA_OK) return rc;
+    if (n == 0 || seqs == 0) return BCA_OK;  // (arrays of no rows may be null)
     if (k_gain && !pos) return BCA_ERR_INVALID_ARGUMENT;
-    if (n == 0 || seqs == 0) return BCA_OK;
     if (!k || !v || !off || !start || !k_pages || !v_pages || (width > 0 && !table)) return BCA_ERR_INVALID_ARGUMENT;
     for (const void *p : {k, v, (const void *)k_pages, (const void *)v_pages})
         if (!aligned(p, 16)) return BCA_ERR_MISALIGNED;
@@ -156,8 +156,8 @@ int bca_paged_attend(bca_paged_t cache, const void *q, int64_t nq, const int32_t
     if (nq > INT32_MAX || width > INT32_MAX / bca::kPage) return BCA_ERR_INVALID_ARGUMENT;
     int rc = on_its_device(c);
     if (rc != BCA_OK) return rc;
+    if (nq == 0 || slices == 0) return BCA_OK;  // (arrays of no rows may be null)
     if (q_gain && !pos) return BCA_ERR_INVALID_ARGUMENT;
-    if (nq == 0 || slices == 0) return BCA_OK;
     if (!q || !k_pages || !v_pages || !off || !k_begin || !k_end || !o || (seqs > 0 && width > 0 && !table))
         return BCA_ERR_INVALID_ARGUMENT;
     if (!workspace && bca::paged_workspace_bytes(c, nq, slices) > 0) return BCA_ERR_INVALID_ARGUMENT;

@@ -32,7 +32,6 @@ struct PagedArgs {
     int seqs, width, slices, causal;
     int hq, hkv, group;
     int rows;             // packed rows of a tile
-    int shares;           // blocks of the attention kernel
     int shift;            // a unit of weight is 16 << shift keys
     int o_fp32;
     float eps;
@@ -47,8 +46,8 @@ struct PagedArgs {
 // A slice's queries are packed token by token, the `group` query heads of a KV head next to
 // one another, and cut into tiles of `rows` packed rows: the rows of a tile read the same
 // keys.  An item is a tile of one KV head.  Items stand in a row (slice, KV head, tile), each
-// as long as its weight, about the keys it reads; block c takes the c-th of `shares` equal
-// stretches of that row.  A stretch that ends inside an item splits the item's pages in
+// as long as its weight, about the keys it reads; block c takes the c-th of kPagedShares
+// equal stretches of that row.  A stretch that ends inside an item splits the item's pages in
 // proportion; the pieces are joined by paged_join_kernel.  So the load is even whatever the
 // lengths are (they are device data), and the cut depends on the arguments alone: the same
 // call gives the same bits.
@@ -123,9 +122,10 @@ __device__ __forceinline__ int32_t paged_limit(const PagedArgs &a, const PagedSl
     return min(s.ke, s.end - (s.n - 1 - token));  // no overflow: both are >= 0 and below 2^31
 }
 
-// Where share c begins in a row of this total weight: total * c / shares.
-__device__ __forceinline__ uint32_t paged_share(uint32_t total, int shares, int c) {
-    const uint32_t n = (uint32_t)shares, x = (uint32_t)c;
+// Where share c begins in a row of this total weight: total * c / kPagedShares.
+__device__ __forceinline__ uint32_t paged_share(uint32_t total, int c) {
+    constexpr uint32_t n = kPagedShares;
+    const uint32_t x = (uint32_t)c;
     return total / n * x + total % n * x / n;
 }
 
@@ -197,8 +197,8 @@ __device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, uint32_t
         sum += mine;
     }
     total = __reduce_add_sync(0xffffffffu, sum);
-    lo = paged_share(total, a.shares, c);
-    hi = paged_share(total, a.shares, c + 1);
+    lo = paged_share(total, c);
+    hi = paged_share(total, c + 1);
     if (lo == hi) return false;
 
     // (offsets that do not rise may make the whole longer than 2^32, and then nothing be found)
@@ -313,9 +313,9 @@ __device__ __forceinline__ void paged_join_of(const PagedArgs &a, const PagedCur
     else if (cur.end() > hi) {
         // the last share that begins before the item ends: an estimate, put right
         const uint32_t end = cur.end();
-        int k = min((int)((float)end / (float)total * a.shares), a.shares - 1);
-        while (k > c && paged_share(total, a.shares, k) >= end) --k;
-        while (k + 1 < a.shares && paged_share(total, a.shares, k + 1) < end) ++k;
+        int k = min((int)((float)end / (float)total * kPagedShares), kPagedShares - 1);
+        while (k > c && paged_share(total, k) >= end) --k;
+        while (k + 1 < kPagedShares && paged_share(total, k + 1) < end) ++k;
         j.last = k;
     }
     a.joins[c] = j;
@@ -496,8 +496,10 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
         if (lane == 0) a.joins[c].last = -1;
         for (int r = lane; r < R; r += 32) paged_part(a, D, 2 * c)[R * D + r] = -INFINITY;
     }
-    // An item is published before the pages of the one before it are loaded, so that its queries
-    // can be made ready meanwhile.
+    // An item is published when the ring's worth of pages of the one before it is on the way, so
+    // that no page waits for it; for the 384-row tiles before those pages, since two warps need the
+    // time of four pages for its queries (ragged chunks: 341 us the other way, 318 us).
+    constexpr bool kEarly = R == kPagedTileRows;
     int published = 0;
     PagedItem x;
     const int32_t *row = nullptr;
@@ -510,7 +512,6 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
         if (more) {
             paged_item(a, cur, c, lo, hi, x);
             row = a.table + (int64_t)cur.s.b * a.width;
-            if (lane == 0 && cur.end() >= hi) paged_join_of(a, cur, x, c, hi, total);
         } else {
             x.p0 = -1;
         }
@@ -525,14 +526,19 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
     while (ok && more) {
         const int32_t p0 = x.p0, p1 = x.p1, g = x.g;
         const int32_t *pages = row;
-        more = cur.end() < hi && cur.next(a);
-        ok = publish();
-        for (int32_t base = p0; base < p1 && ok && !a.skip_loads; base += 32) {
+        const int32_t ahead = kEarly ? p0 : p0 + min(p1 - p0, STAGES);
+        auto next = [&] {
+            if (lane == 0 && cur.end() >= hi) paged_join_of(a, cur, x, c, hi, total);
+            more = cur.end() < hi && cur.next(a);
+            return publish();
+        };
+        if (ahead == p0) ok = next();
+        for (int32_t base = p0; base < p1 && ok; base += 32) {
             const int32_t mine = base + lane < p1 ? __ldg(pages + base + lane) : -1;
             const int count = min(32, p1 - base);
             for (int j = 0; j < count; ++j) {
                 const int32_t page = __shfl_sync(0xffffffffu, mine, j);
-                if (lane == 0 && ok) {
+                if (lane == 0 && ok && !a.skip_loads) {
                     const int st = it % STAGES;
                     if (it >= STAGES) ok = paged_wait(empty(st), (it / STAGES - 1) & 1, a, abort_flag);
                     if (ok) {
@@ -549,6 +555,10 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
                         }
                         ++it;
                     }
+                }
+                if (!kEarly && base + j + 1 == ahead) {
+                    ok = __shfl_sync(0xffffffffu, ok, 0);
+                    if (ok) ok = next();
                 }
             }
             ok = __shfl_sync(0xffffffffu, ok, 0);

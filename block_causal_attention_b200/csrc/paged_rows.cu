@@ -367,7 +367,7 @@ int launch_paged_rows(const PagedCache &c, const PagedArgs &a, cudaStream_t stre
     const void *f = rows_kernel(c, a.rows, bytes);
     PagedArgs args = a;
     void *params[] = {&args};
-    return cudaLaunchKernel(f, dim3((unsigned)a.shares), dim3(kThreads), params, (size_t)bytes, stream) == cudaSuccess
+    return cudaLaunchKernel(f, dim3((unsigned)kPagedShares), dim3(kThreads), params, (size_t)bytes, stream) == cudaSuccess
                ? BCA_OK
                : BCA_ERR_CUDA;
 }

@@ -429,7 +429,9 @@ def test_refusals_of_the_binding():
         PagedCache(4, 2, 48, 6, k_pages=cache.k_pages)       # of a cache with another shape
     # nothing to do is no error
     assert cache.attend(q[:0], table, ref.i32([0, 0]), ref.i32([0]), one).shape == (0, 4, 48)
+    assert cache.attend(q[:0], table, ref.i32([0, 0]), ref.i32([0]), one, pos=pos[:0], q_gain=gain).shape == (0, 4, 48)
     cache.write(k[:0], k[:0], table, ref.i32([0, 0]), ref.i32([0]))
+    cache.write(k[:0], k[:0], table, ref.i32([0, 0]), ref.i32([0]), pos=pos[:0], k_gain=gain)
     cache.close()
     for call in (lambda: cache.attend(**good), lambda: cache.copy_pages([])):
         with pytest.raises(BcaError):
