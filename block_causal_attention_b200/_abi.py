@@ -148,7 +148,7 @@ def lib() -> ctypes.CDLL:
         L.bca_paged_write.restype = i32
         L.bca_paged_copy.argtypes = [vp, vp, i64, vp, vp, vp]
         L.bca_paged_copy.restype = i32
-        L.bca_paged_workspace_bytes.argtypes = [vp, i64, i32]
+        L.bca_paged_workspace_bytes.argtypes = [vp, i64, i32, i32]
         L.bca_paged_workspace_bytes.restype = ctypes.c_size_t
         L.bca_paged_attend.argtypes = [vp, vp, i64, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, vp,
                                        vp, vp]

@@ -282,6 +282,10 @@ int launch_copy(const CopyArgs &a, const PagedCache &c, const int32_t *pairs, in
 // at a time: three trips to memory whatever their number up to 32, and two, four rows a warp,
 // for up to four.
 
+// Calls that a cluster an item takes: up to this many items, tables up to this wide.
+constexpr int kClusterItems = 32;
+constexpr int kClusterPages = 64;
+
 constexpr int kJoinThreads = 256;
 constexpr int kJoinFew = 4;  // pieces that are joined in one go
 
@@ -438,14 +442,19 @@ int by_type(const PagedCache &c, F &&f) {
 //   16-row tiles        33 / 40     57 / 67    106 / 118   203 / 220   397 / 431
 //   32-row tiles        47 / 54     48 / 55     86 / 97    164 / 182   316 / 350
 //   384-row tiles       89 / 111    90 / 112    91 / 114    92 / 116   123 / 155
-int paged_tile_rows(const PagedCache &c, int64_t nq, int slices) {
-    const int64_t rows = nq * (c.hq / c.hkv) / std::max(slices, 1);
-    return rows <= 16 ? 16 : rows <= 64 ? 32 : kPagedTileRows;
+PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices, int width) {
+    const int64_t group = c.hq / c.hkv, rows = nq * group / std::max(slices, 1);
+    PagedShape s = {rows <= 16 ? 16 : rows <= 64 ? 32 : kPagedTileRows, 0};
+    if (s.rows < kPagedTileRows && nq <= kPagedShares && slices <= kPagedShares) {
+        const int64_t items = (nq * group + (int64_t)slices * (s.rows - 1)) / s.rows * c.hkv;
+        if (items <= kClusterItems && width <= kClusterPages) s.items = (int)items;
+    }
+    return s;
 }
 
-size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices) {
-    const size_t rows = (size_t)paged_tile_rows(c, nq, slices);
-    return kPagedShares * (kPagedJoinBytes + 2 * rows * (c.d + 2) * sizeof(float));
+size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices, int width) {
+    const PagedShape s = paged_shape(c, nq, slices, width);
+    return s.items > 0 ? 0 : kPagedShares * (kPagedJoinBytes + 2 * (size_t)s.rows * (c.d + 2) * sizeof(float));
 }
 
 int prepare_paged(const PagedCache &c) {
@@ -538,7 +547,8 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
     a.hq = c.hq;
     a.hkv = c.hkv;
     a.group = c.hq / c.hkv;
-    a.rows = paged_tile_rows(c, io.nq, io.slices);
+    const PagedShape s = paged_shape(c, io.nq, io.slices, io.width);
+    a.rows = s.rows;
     a.o_fp32 = (c.flags & BCA_O_FP32) ? 1 : 0;
     a.eps = c.eps;
     a.scale = 1.4426950408889634f / std::sqrt((float)c.d);
@@ -551,8 +561,9 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
     a.shift = 0;
     while (a.shift < 27 && items * (64.0 + std::ldexp(keys, -4 - a.shift)) > 2e9) ++a.shift;
     if (items * 65.0 > 2e9) return BCA_ERR_TOO_LARGE;
-    const int rc = a.rows == kPagedTileRows ? launch_paged_tiles(c, a, stream) : launch_paged_rows(c, a, stream);
-    if (rc != BCA_OK) return rc;
+    const int rc =
+        a.rows == kPagedTileRows ? launch_paged_tiles(c, a, stream) : launch_paged_rows(c, a, s.items, stream);
+    if (rc != BCA_OK || s.items > 0) return rc;
     return by_type(c, [&](auto d, auto t) { return launch_join<decltype(d)::value, decltype(t)>(a, stream); });
 }
 

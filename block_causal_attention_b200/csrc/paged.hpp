@@ -59,10 +59,15 @@ struct PagedAttendIO {
     void *workspace;
 };
 
-// Packed (token, head of the KV group) rows of the tiles that a call of these sizes is cut into
-// (the same for the workspace and the launch).
-int paged_tile_rows(const PagedCache &c, int64_t nq, int slices);
-size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices);
+// How a call of these sizes is cut (the same for the workspace and the launch): tiles of `rows`
+// packed (token, head of the KV group) rows; items > 0: that many (tile, KV head) items, a cluster
+// of blocks each; 0: equal shares of whatever there is.
+struct PagedShape {
+    int rows;
+    int items;
+};
+PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices, int width);
+size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices, int width);
 
 int prepare_paged(const PagedCache &c);
 int launch_paged_write(const PagedCache &c, const PagedWriteIO &io, cudaStream_t stream);
@@ -72,7 +77,7 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
 
 struct PagedArgs;
 int prepare_paged_rows(const PagedCache &c);
-int launch_paged_rows(const PagedCache &c, const PagedArgs &a, cudaStream_t stream);
+int launch_paged_rows(const PagedCache &c, const PagedArgs &a, int items, cudaStream_t stream);
 int prepare_paged_tiles(const PagedCache &c);
 int launch_paged_tiles(const PagedCache &c, const PagedArgs &a, cudaStream_t stream);
 

@@ -142,9 +142,9 @@ int bca_paged_copy(bca_paged_t cache, const int32_t *pairs, int64_t n, void *k_p
     return bca::launch_paged_copy(c, pairs, n, k_pages, v_pages, static_cast<cudaStream_t>(stream));
 }
 
-size_t bca_paged_workspace_bytes(bca_paged_t cache, int64_t nq, int32_t slices) {
-    if (!cache || nq <= 0 || slices <= 0) return 0;
-    return bca::paged_workspace_bytes(cache->cache, nq, slices);
+size_t bca_paged_workspace_bytes(bca_paged_t cache, int64_t nq, int32_t slices, int32_t width) {
+    if (!cache || nq <= 0 || slices <= 0 || width < 0) return 0;
+    return bca::paged_workspace_bytes(cache->cache, nq, slices, width);
 }
 
 int bca_paged_attend(bca_paged_t cache, const void *q, int64_t nq, const int32_t *pos, const float *q_gain,
@@ -160,7 +160,7 @@ int bca_paged_attend(bca_paged_t cache, const void *q, int64_t nq, const int32_t
     if (q_gain && !pos) return BCA_ERR_INVALID_ARGUMENT;
     if (!q || !k_pages || !v_pages || !off || !k_begin || !k_end || !o || (seqs > 0 && width > 0 && !table))
         return BCA_ERR_INVALID_ARGUMENT;
-    if (!workspace && bca::paged_workspace_bytes(c, nq, slices) > 0) return BCA_ERR_INVALID_ARGUMENT;
+    if (!workspace && bca::paged_workspace_bytes(c, nq, slices, width) > 0) return BCA_ERR_INVALID_ARGUMENT;
     for (const void *p : {q, k_pages, v_pages, (const void *)o, (const void *)workspace})
         if (!aligned(p, 16)) return BCA_ERR_MISALIGNED;
     for (const void *p : {(const void *)pos, (const void *)q_gain, (const void *)table, (const void *)off,

@@ -226,17 +226,19 @@ PyObject *attend(PyObject *, PyObject *const *a, Py_ssize_t n) {
         if (current.stream() != stream)
             guard.emplace(c10::cuda::getStreamFromExternal(stream, (c10::DeviceIndex)c->device));
         at::Tensor o, workspace;
-        void *op, *ws;
+        void *op, *ws = nullptr;
         if (a[11] == Py_None) {
             o = empty_on(*c, {nq, c->hq, c->d}, c->o_dtype);
             op = o.data_ptr();
         } else {
             op = tensor(*c, "o", a[11], c->o_dtype, {nq, c->hq, c->d});
         }
-        const int64_t bytes = (int64_t)bca_paged_workspace_bytes(c->handle, nq, (int32_t)slices);
+        const int64_t bytes = (int64_t)bca_paged_workspace_bytes(c->handle, nq, (int32_t)slices, (int32_t)width);
         if (a[13] == Py_None) {
-            workspace = empty_on(*c, {std::max<int64_t>(bytes, 16)}, at::kByte);
-            ws = workspace.data_ptr();
+            if (bytes > 0) {
+                workspace = empty_on(*c, {bytes}, at::kByte);
+                ws = workspace.data_ptr();
+            }
         } else {
             if (!THPVariable_Check(a[13])) {
                 PyErr_SetString(PyExc_TypeError, "workspace: expected a tensor");

@@ -257,6 +257,36 @@ __device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, uint32_t
     return true;
 }
 
+// Calls of few items over short rows: a cluster of kCluster blocks has an item, the pages in equal
+// parts, and joins the parts over distributed shared memory: no shares, no second launch.  Slice i
+// has the item slots from (off[i] * group + i (R - 1)) / R on, of each KV head: room for its
+// ceil(n * group / R) tiles before the next slice's begin, whatever the offsets are.
+constexpr int kCluster = 8;
+
+template <int R>
+__device__ __forceinline__ bool paged_locate_item(const PagedArgs &a, int item, PagedCursor<R> &cur) {
+    const int lane = threadIdx.x & 31;
+    const uint32_t y = (uint32_t)item / (uint32_t)a.hkv;
+    auto first = [&](int i) {
+        const uint32_t o = (uint32_t)min(max(__ldg(a.off + i), 0), (int32_t)a.nq);
+        return (o * (uint32_t)a.group + (uint32_t)i * (R - 1)) / R;
+    };
+    int count = 0;
+    for (int base = 0; base < a.slices; base += 32) {
+        const bool before = base + lane < a.slices && first(base + lane) <= y;
+        const uint32_t m = __ballot_sync(0xffffffffu, before);
+        count += __popc(m);
+        if (m != 0xffffffffu) break;
+    }
+    if (count == 0) return false;
+    cur.slice = count - 1;
+    cur.s = paged_slice<R>(a, cur.slice);
+    cur.g = (int32_t)((uint32_t)item - y * (uint32_t)a.hkv);
+    cur.t = y - first(cur.slice);
+    cur.start = 0;
+    return cur.t < cur.s.tiles;
+}
+
 // What the warps of a block need to know of the item they are at: written by the warp that
 // walks the row of items (and loads their pages), a few items ahead, so that the others
 // neither hold a cursor in registers nor wait for the loads of the next slice.
@@ -475,12 +505,12 @@ __device__ __forceinline__ bool paged_wait(uint32_t bar, uint32_t parity, const 
     return false;
 }
 
-// The warp that walks the items of share c: publishes each and moves its pages into the ring, a page's
+// The warp that walks the items of share c (CL > 1: that has item c / CL, part c % CL): publishes each and moves its pages into the ring, a page's
 // keys and values by one bulk copy each, until the block's stretch ends; then waits for the
 // copies that are still in flight.  Barriers: full / empty of the STAGES page stages (base +
 // 8 i, base + 8 (STAGES + i)), and of the kItemRing items behind them.  here[i]: stage i holds
 // a page; an absent one holds no keys.
-template <int R, int STAGES, int TILE, int KSTAGE, int STAGE>
+template <int R, int STAGES, int TILE, int KSTAGE, int STAGE, int CL = 1>
 __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t ring, uint32_t bars, uint32_t item_bars, PagedItem *items,
                                            volatile int *here, volatile int *abort_flag) {
     const int lane = threadIdx.x & 31;
@@ -490,8 +520,10 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
     PagedCursor<R> cur;
     uint32_t lo, hi, total;
     int it = 0;
-    bool more = paged_locate(a, c, lo, hi, total, cur);
-    if (!more) {
+    bool more;
+    if constexpr (CL > 1) more = paged_locate_item(a, c / CL, cur);
+    else more = paged_locate(a, c, lo, hi, total, cur);
+    if (CL == 1 && !more) {
         // an empty stretch inside an item that others share: a piece without keys
         if (lane == 0) a.joins[c].last = -1;
         for (int r = lane; r < R; r += 32) paged_part(a, D, 2 * c)[R * D + r] = -INFINITY;
@@ -510,7 +542,14 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
                                                 (published / kItemRing - 1) & 1, a, abort_flag)))
             return false;
         if (more) {
-            paged_item(a, cur, c, lo, hi, x);
+            if constexpr (CL > 1) {
+                paged_item(a, cur, 0, 0, cur.end(), x);
+                const int32_t np = x.p1 - x.p0, rank = c % CL;
+                x.p1 = x.p0 + (int32_t)((int64_t)np * (rank + 1) / CL);
+                x.p0 += (int32_t)((int64_t)np * rank / CL);
+            } else {
+                paged_item(a, cur, c, lo, hi, x);
+            }
             row = a.table + (int64_t)cur.s.b * a.width;
         } else {
             x.p0 = -1;
@@ -528,8 +567,12 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
         const int32_t *pages = row;
         const int32_t ahead = kEarly ? p0 : p0 + min(p1 - p0, STAGES);
         auto next = [&] {
-            if (lane == 0 && cur.end() >= hi) paged_join_of(a, cur, x, c, hi, total);
-            more = cur.end() < hi && cur.next(a);
+            if constexpr (CL > 1) {
+                more = false;
+            } else {
+                if (lane == 0 && cur.end() >= hi) paged_join_of(a, cur, x, c, hi, total);
+                more = cur.end() < hi && cur.next(a);
+            }
             return publish();
         };
         if (ahead == p0) ok = next();
@@ -564,7 +607,7 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
             ok = __shfl_sync(0xffffffffu, ok, 0);
         }
     }
-    if (!ok && lane == 0) a.joins[c].last = -1;
+    if (CL == 1 && !ok && lane == 0) a.joins[c].last = -1;
     // every copy must have landed before the block may end
     if (lane == 0)
         for (int j = it > STAGES ? it - STAGES : 0; j < it; ++j)

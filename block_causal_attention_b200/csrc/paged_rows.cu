@@ -31,15 +31,17 @@ constexpr int kWarps = 8;                     // consumers; one more fills the r
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kWarpTokens = kPage / kWarps;   // 16
 
-template <int D>
+template <int D, int MT, int CL>
 struct RowsSmem {
     static constexpr int TILE = D * kPage * 2;
-    static constexpr int STAGES = D == 48 ? 7 : D == 32 ? 10 : 13;
+    // one block a multiprocessor with all of its shared memory; of a cluster's blocks two
+    static constexpr int STAGES = CL == 1 ? (D == 48 ? 7 : D == 32 ? 10 : 13) : (D == 48 ? 3 : D == 32 ? 5 : 6);
     static constexpr int QSTRIDE = D == 24 ? 40 : D + 8;  // elements; an odd number of 16-byte units
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_Q = STAGES * 2 * TILE;
-    static constexpr int OFF_MERGE = OFF_Q + 32 * QSTRIDE * 2;
-    static constexpr int OFF_BAR = OFF_MERGE + kWarps * 16 * (D + 2) * 4;
+    static constexpr int OFF_MERGE = OFF_Q + 16 * MT * QSTRIDE * 2;
+    static constexpr int OFF_PART = OFF_MERGE + kWarps * 16 * (D + 2) * 4;  // the block's, for its cluster
+    static constexpr int OFF_BAR = OFF_PART + (CL == 1 ? 0 : 16 * MT * (D + 2) * 4);
     static constexpr int OFF_HERE = OFF_BAR + 2 * (STAGES + kItemRing) * 8;
     static constexpr int OFF_ITEMS = OFF_HERE + STAGES * 4;
     static constexpr int OFF_ABORT = OFF_ITEMS + kItemRing * (int)sizeof(PagedItem);
@@ -61,10 +63,23 @@ __device__ __forceinline__ bool consumers_all(bool yes) {
     return all != 0;
 }
 
-// MT: 16-row matrix tiles a work tile has (rows = 16 MT).
-template <int D, typename T, int MT>
+__device__ __forceinline__ void cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// A word of the shared memory of the cluster's block `rank`, at this block's address of it.
+__device__ __forceinline__ float cluster_load(uint32_t addr, int rank) {
+    uint32_t there;
+    float x;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(there) : "r"(addr), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(x) : "r"(there) : "memory");
+    return x;
+}
+
+// MT: 16-row matrix tiles a work tile has (rows = 16 MT).  CL: blocks that share an item as a
+// cluster; 1: the blocks take equal shares of all items.
+template <int D, typename T, int MT, int CL>
 __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_constant__ PagedArgs a) {
-    using L = RowsSmem<D>;
+    using L = RowsSmem<D, MT, CL>;
     constexpr int S = L::STAGES;
     constexpr int R = 16 * MT;
     constexpr int KS = D / 16;            // 16-channel steps; D = 24 has an 8-channel one behind
@@ -83,7 +98,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
 
     // the joining kernel may be put in place as blocks of this one end
-    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if constexpr (CL == 1) asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if (threadIdx.x == 0) {
         *abort_flag = 0;
         for (int i = 0; i < S; ++i) {
@@ -100,7 +115,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     __syncthreads();
 
     if (warp == kWarps) {
-        paged_fill<R, S, L::TILE, L::TILE, 2 * L::TILE>(a, c, sbase + L::OFF_RING, full(0), item_bars, items,
+        paged_fill<R, S, L::TILE, L::TILE, 2 * L::TILE, CL>(a, c, sbase + L::OFF_RING, full(0), item_bars, items,
                                                      here, abort_flag);
         return;
     }
@@ -115,6 +130,25 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     const uint32_t vaddr = ((2 * warp + (lane >> 3 & 1)) * D + 8 * (lane >> 4) + (lane & 7)) * 16;
     float2 gain[Row8<D>::N];
     Row8<D>::load_gain(a.q_gain, lane & 7, gain);
+    // O / l and the LSE of row r of an item: channels e, e + 16, .. of 16 lanes
+    auto write = [&](const PagedItem &x, int r, int e, float top, float l, const float (&y)[(D + 15) / 16]) {
+        const bool none = top == -INFINITY;
+        const float inv = none ? 0.f : 1.f / l;
+        const uint32_t packed = x.head + r;
+        const int64_t token = x.row + x.token + (int32_t)(packed / a.group);
+        const int head = x.g * a.group + (int)(packed % a.group);
+        const int64_t at = (token * a.hq + head) * D;
+#pragma unroll
+        for (int i = 0; i < (D + 15) / 16; ++i) {
+            if (e + 16 * i >= D) continue;
+            const float z = none ? 0.f : y[i] * inv;
+            if (a.o_fp32) static_cast<float *>(a.o)[at + e + 16 * i] = z;
+            else static_cast<T *>(a.o)[at + e + 16 * i] = T(z);
+        }
+        if (a.lse && e == 0) a.lse[head * a.nq + token] = none ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+    };
+    PagedItem mine;    // of a cluster
+    bool has = false;
     bool ok = true;
     int it = 0;
     for (int n_item = 0;; ++n_item) {
@@ -264,13 +298,13 @@ ldsm_v<NV>(vs + vaddr, vf);
         // ------------------------------------------------ the eight warps' results meet
 #pragma unroll
         for (int m = 0; m < MT; ++m) {
-            float *mine = merge + warp * 16 * (D + 2);
+            float *own = merge + warp * 16 * (D + 2);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 float l = sum[m][h];
                 l += __shfl_xor_sync(0xffffffffu, l, 1);
                 l += __shfl_xor_sync(0xffffffffu, l, 2);
-                float *row = mine + (g + 8 * h) * (D + 2);
+                float *row = own + (g + 8 * h) * (D + 2);
 #pragma unroll
                 for (int n = 0; n < NV; ++n)
                     *reinterpret_cast<float2 *>(row + 8 * n + 2 * t) = make_float2(o[m][n][2 * h], o[m][n][2 * h + 1]);
@@ -295,24 +329,18 @@ ldsm_v<NV>(vs + vaddr, vf);
                 for (int i = 0; i < (D + 15) / 16; ++i)
                     if (e + 16 * i < D) y[i] = fmaf(in[e + 16 * i], mul, y[i]);
             }
-            if (16 * m + r < x.left) {
-                if (x.whole) {
-                    const bool none = top == -INFINITY;
-                    const float inv = none ? 0.f : 1.f / l;
-                    const uint32_t packed = x.head + 16 * m + r;
-                    const int64_t token = x.row + x.token + (int32_t)(packed / a.group);
-                    const int head = x.g * a.group + (int)(packed % a.group);
-                    const int64_t at = (token * a.hq + head) * D;
+            if constexpr (CL > 1) {
+                float *part = reinterpret_cast<float *>(smem + L::OFF_PART) + (16 * m + r) * (D + 2);
 #pragma unroll
-                    for (int i = 0; i < (D + 15) / 16; ++i) {
-                        if (e + 16 * i >= D) continue;
-                        const float z = none ? 0.f : y[i] * inv;
-                        if (a.o_fp32) static_cast<float *>(a.o)[at + e + 16 * i] = z;
-                        else static_cast<T *>(a.o)[at + e + 16 * i] = T(z);
-                    }
-                    if (a.lse && e == 0)
-                        a.lse[head * a.nq + token] =
-                            none ? -INFINITY : (top + log2f(l)) * 0.69314718055994531f;
+                for (int i = 0; i < (D + 15) / 16; ++i)
+                    if (e + 16 * i < D) part[e + 16 * i] = y[i];
+                if (e == 0) {
+                    part[D] = top;
+                    part[D + 1] = l;
+                }
+            } else if (16 * m + r < x.left) {
+                if (x.whole) {
+                    write(x, 16 * m + r, e, top, l, y);
                 } else {  // without pages too: the reference, -inf, tells
                     float *part = paged_part(a, D, x.part);
 #pragma unroll
@@ -326,50 +354,102 @@ ldsm_v<NV>(vs + vaddr, vf);
             }
             consumers_sync();
         }
+        if constexpr (CL > 1) {
+            has = true;
+            mine = x;
+        }
         if (lane == 0) mbar_arrive(item_bars + 8u * (kItemRing + slot));
+    }
+    if constexpr (CL > 1) {
+        // Every block comes through both barriers, also one that had nothing to do or gave up: the
+        // others read its memory in between.
+        __syncwarp();
+        cluster_sync();
+        if (has) {
+            const int r = c % CL * (R / CL) + (threadIdx.x >> 4), e = threadIdx.x & 15;
+            if (threadIdx.x < 16 * (R / CL) && r < mine.left) {
+                const uint32_t part = sbase + L::OFF_PART + r * (D + 2) * 4;
+                float ref[CL], l[CL], in[CL][(D + 15) / 16];
+#pragma unroll
+                for (int k = 0; k < CL; ++k) {
+                    ref[k] = cluster_load(part + D * 4, k);
+                    l[k] = cluster_load(part + (D + 1) * 4, k);
+#pragma unroll
+                    for (int i = 0; i < (D + 15) / 16; ++i)
+                        in[k][i] = cluster_load(part + min(e + 16 * i, D - 1) * 4, k);
+                }
+                float top = ref[0], sum = 0.f, y[(D + 15) / 16] = {};
+#pragma unroll
+                for (int k = 1; k < CL; ++k) top = fmaxf(top, ref[k]);
+#pragma unroll
+                for (int k = 0; k < CL; ++k) {
+                    const float mul = top == -INFINITY ? 0.f : ex2(ref[k] - top);
+                    sum = fmaf(l[k], mul, sum);
+#pragma unroll
+                    for (int i = 0; i < (D + 15) / 16; ++i) y[i] = fmaf(in[k][i], mul, y[i]);
+                }
+                write(mine, r, e, top, sum, y);
+            }
+        }
+        __syncwarp();
+        cluster_sync();
     }
 }
 
 template <int D, typename T>
-const void *rows_kernel(int rows) {
-    return rows == 16 ? (const void *)paged_rows_kernel<D, T, 1> : (const void *)paged_rows_kernel<D, T, 2>;
+const void *rows_kernel(int rows, bool cluster) {
+    if (cluster)
+        return rows == 16 ? (const void *)paged_rows_kernel<D, T, 1, kCluster>
+                          : (const void *)paged_rows_kernel<D, T, 2, kCluster>;
+    return rows == 16 ? (const void *)paged_rows_kernel<D, T, 1, 1> : (const void *)paged_rows_kernel<D, T, 2, 1>;
 }
 
-const void *rows_kernel(const PagedCache &c, int rows, int &bytes) {
+template <int D>
+const void *rows_kernel(bool f16, int rows, bool cluster, int &bytes) {
+    bytes = cluster ? (rows == 16 ? RowsSmem<D, 1, kCluster>::BYTES : RowsSmem<D, 2, kCluster>::BYTES)
+                    : (rows == 16 ? RowsSmem<D, 1, 1>::BYTES : RowsSmem<D, 2, 1>::BYTES);
+    return f16 ? rows_kernel<D, __half>(rows, cluster) : rows_kernel<D, __nv_bfloat16>(rows, cluster);
+}
+
+const void *rows_kernel(const PagedCache &c, int rows, bool cluster, int &bytes) {
     const bool f16 = (c.flags & BCA_PAGED_FP16) != 0;
     switch (c.d) {
-        case 24:
-            bytes = RowsSmem<24>::BYTES;
-            return f16 ? rows_kernel<24, __half>(rows) : rows_kernel<24, __nv_bfloat16>(rows);
-        case 32:
-            bytes = RowsSmem<32>::BYTES;
-            return f16 ? rows_kernel<32, __half>(rows) : rows_kernel<32, __nv_bfloat16>(rows);
-        default:
-            bytes = RowsSmem<48>::BYTES;
-            return f16 ? rows_kernel<48, __half>(rows) : rows_kernel<48, __nv_bfloat16>(rows);
+        case 24: return rows_kernel<24>(f16, rows, cluster, bytes);
+        case 32: return rows_kernel<32>(f16, rows, cluster, bytes);
+        default: return rows_kernel<48>(f16, rows, cluster, bytes);
     }
 }
 
 }  // namespace
 
 int prepare_paged_rows(const PagedCache &c) {
-    for (int rows : {16, 32}) {
-        int bytes = 0;
-        const void *f = rows_kernel(c, rows, bytes);
-        if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-            return BCA_ERR_CUDA;
-    }
+    for (int rows : {16, 32})
+        for (bool cluster : {false, true}) {
+            int bytes = 0;
+            const void *f = rows_kernel(c, rows, cluster, bytes);
+            if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+                return BCA_ERR_CUDA;
+        }
     return BCA_OK;
 }
 
-int launch_paged_rows(const PagedCache &c, const PagedArgs &a, cudaStream_t stream) {
+int launch_paged_rows(const PagedCache &c, const PagedArgs &a, int items, cudaStream_t stream) {
     int bytes = 0;
-    const void *f = rows_kernel(c, a.rows, bytes);
+    const void *f = rows_kernel(c, a.rows, items > 0, bytes);
     PagedArgs args = a;
     void *params[] = {&args};
-    return cudaLaunchKernel(f, dim3((unsigned)kPagedShares), dim3(kThreads), params, (size_t)bytes, stream) == cudaSuccess
-               ? BCA_OK
-               : BCA_ERR_CUDA;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(items > 0 ? items * kCluster : kPagedShares));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = (size_t)bytes;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr = {};
+    attr.id = cudaLaunchAttributeClusterDimension;
+    attr.val.clusterDim.x = kCluster;
+    attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = items > 0 ? 1 : 0;
+    return cudaLaunchKernelExC(&cfg, f, params) == cudaSuccess ? BCA_OK : BCA_ERR_CUDA;
 }
 
 }  // namespace bca

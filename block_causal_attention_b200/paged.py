@@ -138,13 +138,14 @@ class PagedCache:
             _abi.check(o, "bca_paged_attend")
         return o
 
-    def workspace_bytes(self, nq: int, slices: int) -> int:
-        return int(self._lib.bca_paged_workspace_bytes(self._h, nq, slices))
+    def workspace_bytes(self, nq: int, slices: int, width: int) -> int:
+        """Bytes of workspace of an ``attend`` call: rows of q, slices, columns of the table."""
+        return int(self._lib.bca_paged_workspace_bytes(self._h, nq, slices, width))
 
-    def alloc_workspace(self, nq: int, slices: int, stream=None):
+    def alloc_workspace(self, nq: int, slices: int, width: int, stream=None):
         """Workspace of an ``attend`` call of these sizes, on its stream.  Calls that may overlap
         on the GPU (two streams, two captured graphs replayed side by side) need one each."""
-        n = max(16, self.workspace_bytes(nq, slices))
+        n = max(16, self.workspace_bytes(nq, slices, width))
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
         with torch.cuda.stream(stream):   # its next user is behind this call; None: the current one

@@ -419,10 +419,10 @@ int bca_paged_copy(bca_paged_t cache, const int32_t *pairs, int64_t n, void *k_p
  *   lse    : fp32 [Hq][nq] natural log, or NULL (not wanted)
  * Rows that see no key get O = 0 and LSE = -inf; rows of q outside every slice are neither
  * read nor written.  What pages hold outside a row's own keys never reaches the row, NaN and
- * infinities included.  workspace: bca_paged_workspace_bytes bytes, 16-byte aligned; calls
- * that may overlap on the GPU need one each.  Results do not depend on timing: the same call
+ * infinities included.  workspace: bca_paged_workspace_bytes bytes (which may be 0: NULL then),
+ * 16-byte aligned; calls that may overlap on the GPU need one each.  Results do not depend on timing: the same call
  * gives the same bits. */
-size_t bca_paged_workspace_bytes(bca_paged_t cache, int64_t nq, int32_t slices);
+size_t bca_paged_workspace_bytes(bca_paged_t cache, int64_t nq, int32_t slices, int32_t width);
 int bca_paged_attend(bca_paged_t cache, const void *q, int64_t nq, const int32_t *pos, const float *q_gain,
                      const void *k_pages, const void *v_pages, const int32_t *table, int32_t seqs,
                      int32_t width, const int32_t *off, const int32_t *seq, const int32_t *k_begin,

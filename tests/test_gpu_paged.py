@@ -35,6 +35,13 @@ def no_worse(got, want, bound, what):
                           f"first at {bad.nonzero()[0].tolist()}"
 
 
+def widened(table):
+    """The same table with absent pages behind it, to 200 columns."""
+    wide = torch.full((table.shape[0], max(200, table.shape[1])), -1, dtype=torch.int32, device="cuda")
+    wide[:, :table.shape[1]] = table
+    return wide
+
+
 def check_attend(hq, hkv, d, dtype, new, ctx, causal, prologue, seed, block=0, kv_range=0, o_fp32=False, far=100):
     g = gen(seed)
     need = [-(-(n + c) // PAGE) for n, c in zip(new, ctx)]
@@ -56,12 +63,15 @@ def check_attend(hq, hkv, d, dtype, new, ctx, causal, prologue, seed, block=0, k
     o = torch.full((nq, hq, d), math.nan, dtype=torch.float32 if o_fp32 else dtype, device="cuda")
     lse = torch.full((hq, nq), math.nan, device="cuda")
     seq, kb, ke = [x[0] for x in sl], [x[2] for x in sl], [x[3] for x in sl]
-    cache.attend(q, table, ref.i32(off), ref.i32(kb), ref.i32(ke), seq=ref.i32(seq), causal=causal, pos=pos,
-                 q_gain=gain, o=o, lse=lse)
-    assert cache.status() == _abi.BCA_OK
     wo, wl, bo, bl = ref.attend(q, kp[0], vp[0], table, off, seq, kb, ke, causal, pos, gain)
-    no_worse(o, wo, bo, "o")
-    no_worse(lse, wl, bl, "lse")
+    for tab in (table, widened(table)):          # few items go by clusters, or by shares where tables are wide
+        o.fill_(math.nan)
+        lse.fill_(math.nan)
+        cache.attend(q, tab, ref.i32(off), ref.i32(kb), ref.i32(ke), seq=ref.i32(seq), causal=causal, pos=pos,
+                     q_gain=gain, o=o, lse=lse)
+        assert cache.status() == _abi.BCA_OK
+        no_worse(o, wo, bo, "o")
+        no_worse(lse, wl, bl, "lse")
 
 
 # ---------------------------------------------------------------------------------- write
@@ -218,7 +228,10 @@ def test_attend_empty_slices_and_rows_left_alone(rows, dtype):
     q = rand((nq, 4, 48), dtype, g)
     o = torch.full((nq, 4, 48), 7.0, dtype=dtype, device="cuda")
     lse = torch.full((4, nq), 7.0, device="cuda")
-    for causal in (False, True):
+    for causal, wide in ((False, False), (True, False), (False, True), (True, True)):
+        if wide:
+            ke[6] = 30000                        # keys behind the wider table too
+            table = widened(table)
         cache.attend(q, table, ref.i32(off), ref.i32(kb), ref.i32(ke), seq=ref.i32(seq), causal=causal, o=o, lse=lse)
         assert cache.status() == _abi.BCA_OK
         wo, wl, bo, bl = ref.attend(q, kp[0], vp[0], table, off, seq, kb, ke, causal)
@@ -253,8 +266,8 @@ def test_attend_what_a_row_does_not_see_does_not_reach_it(rows, dtype, d):
         cache = PagedCache(hq, hkv, d, 5, dtype=dtype, k_pages=kp, v_pages=vp)
         q = rand((rows, hq, d), dtype, g)
         o, lse = torch.empty_like(q), torch.empty((hq, rows), device="cuda")
-        for causal in (True, False):
-            cache.attend(q, table, ref.i32([0, rows]), ref.i32([kb]), ref.i32([end]), causal=causal, o=o, lse=lse)
+        for causal, tab in ((True, table), (False, table), (True, widened(table)), (False, widened(table))):
+            cache.attend(q, tab, ref.i32([0, rows]), ref.i32([kb]), ref.i32([end]), causal=causal, o=o, lse=lse)
             assert cache.status() == _abi.BCA_OK
             wo, wl, bo, bl = ref.attend(q, kp[0], vp[0], table, [0, rows], [0], [kb], [end], causal)
             assert wo.isnan().any() or wo.isinf().any()
@@ -283,9 +296,9 @@ def test_attend_any_offsets_stay_inside():
                                  ([0, big, -big], [big, -big], [0, 0], [big, big]),
                                  ([-big, big, big], [0, 1], [-big, big], [big, -big])):
             for causal in (False, True):
-                cache.attend(q, ref.i32([[0, big, 1], [-big, 2, 4]]), ref.i32(off), ref.i32(kb), ref.i32(ke),
-                             seq=ref.i32(seq), causal=causal, o=o)
-                assert cache.status() == _abi.BCA_OK
+                for tab in (ref.i32([[0, big, 1], [-big, 2, 4]]), widened(ref.i32([[0, big, 1], [-big, 2, 4]]))):
+                    cache.attend(q, tab, ref.i32(off), ref.i32(kb), ref.i32(ke), seq=ref.i32(seq), causal=causal, o=o)
+                    assert cache.status() == _abi.BCA_OK
         assert (raw[:32] == 3).all() and (raw[32 + rows:] == 3).all()
         kv = rand((rows, 2, 32), BF, g)
         for off, at in (([5, 0, 9], [0, 0]), ([-4, 2, big], [big, -big]), ([-big, big, big], [0, 5])):
@@ -300,7 +313,7 @@ def test_attend_same_bits_again_and_on_another_stream():
     cache = PagedCache(16, 2, 48, 60, k_pages=kp, v_pages=vp)
     for n in (1, 3, 300):
         q = rand((2 * n, 16, 48), BF, g)
-        args = (q, table, ref.i32([0, n, 2 * n]), ref.i32([0, 5]), ref.i32([6001, 1100]))
+        args = (q, table if n != 3 else widened(table), ref.i32([0, n, 2 * n]), ref.i32([0, 5]), ref.i32([6001, 1100]))
         first = cache.attend(*args, causal=True)
         torch.cuda.synchronize()
         s = torch.cuda.Stream()
@@ -325,7 +338,7 @@ def test_captured_step_replays_for_other_lengths(most):
     table, off = ref.i32([[0] * 8] * 3), ref.i32([0] * 4)
     kb, ke, start, pos = ref.i32([0] * 3), ref.i32([0] * 3), ref.i32([0] * 3), positions(nq, g)
     o = torch.zeros_like(q)
-    ws = cache.alloc_workspace(nq, 3)
+    ws = cache.alloc_workspace(nq, 3, 8)
 
     def step():
         cache.write(k, v, table, off, start, pos=pos)
@@ -354,7 +367,7 @@ def test_workspace_and_outputs_are_not_overrun():
     for n, hq, hkv, d in ((1, 16, 1, 24), (2, 12, 1, 48), (3, 16, 1, 32), (100, 8, 2, 48)):
         kp, vp = ref.pools(30, hkv, d, BF, g)
         cache = PagedCache(hq, hkv, d, 30, k_pages=kp, v_pages=vp)
-        table = ref.table_of([30], 30, g)
+        table = widened(ref.table_of([30], 30, g))
         raw = []
 
         def guarded(shape, dtype):
@@ -363,7 +376,7 @@ def test_workspace_and_outputs_are_not_overrun():
             raw.append((r, bytes_))
             return r[4096:4096 + bytes_].view(dtype).view(shape)
         o, lse = guarded((n, hq, d), BF), guarded((hq, n), torch.float32)
-        ws = guarded((cache.workspace_bytes(n, 1),), torch.uint8)
+        ws = guarded((cache.workspace_bytes(n, 1, 200),), torch.uint8)
         cache.attend(rand((n, hq, d), BF, g), table, ref.i32([0, n]), ref.i32([0]), ref.i32([30 * PAGE]), causal=True,
                      o=o, lse=lse, workspace=ws)
         assert cache.status() == _abi.BCA_OK
@@ -371,11 +384,12 @@ def test_workspace_and_outputs_are_not_overrun():
             assert (r[:4096] == 0xA5).all() and (r[4096 + b:] == 0xA5).all()
 
 
-@pytest.mark.parametrize("rows", [1, 200])
-def test_forced_timeout_is_reported_and_the_context_stays_usable(rows):
+@pytest.mark.parametrize("rows,wide", [(1, False), (1, True), (200, False)])
+def test_forced_timeout_is_reported_and_the_context_stays_usable(rows, wide):
     g = gen(15)
     kp, vp = ref.pools(4, 2, 48, BF, g)
     table = ref.table_of([4], 4, g)
+    table = widened(table) if wide else table
     q = rand((rows, 16, 48), BF, g)
     args = (q, table, ref.i32([0, rows]), ref.i32([0]), ref.i32([512]))
     bad = PagedCache(16, 2, 48, 4, k_pages=kp, v_pages=vp, test_force_timeout=True)
@@ -409,11 +423,12 @@ def test_refusals_of_the_binding():
     good = dict(q=q, table=table, off=off, k_begin=ref.i32([0]), k_end=one, seq=ref.i32([0]), pos=pos, q_gain=gain)
     o = cache.attend(**good)
     assert o.dtype is BF and o.shape == (5, 4, 48)
-    small = torch.empty(cache.workspace_bytes(5, 1) - 1, dtype=torch.uint8, device="cuda")
+    small = torch.empty(cache.workspace_bytes(5, 1, 200) - 1, dtype=torch.uint8, device="cuda")
+    wide = torch.full((1, 200), -1, dtype=torch.int32, device="cuda")
     for bad in (dict(q=q.half()), dict(q=q[:, :3]), dict(q=q[:4]), dict(table=table.cpu()), dict(off=off.long()),
                 dict(k_begin=off), dict(k_end=one.cpu()), dict(seq=off), dict(pos=None), dict(q_gain=gain.double()),
-                dict(o=o.float()), dict(o=o[:3]), dict(lse=torch.empty(4, 4, device="cuda")), dict(workspace=small),
-                dict(workspace=small.cpu()), dict(layer=2), dict(off=off[:0]),
+                dict(o=o.float()), dict(o=o[:3]), dict(lse=torch.empty(4, 4, device="cuda")), dict(table=wide, workspace=small),
+                dict(table=wide, workspace=small.cpu()), dict(layer=2), dict(off=off[:0]),
                 dict(table=ref.i32([[0, 1], [2, 3]]), seq=None)):
         with pytest.raises(ValueError):
             cache.attend(**{**good, **bad})
@@ -443,7 +458,8 @@ def test_allocations_of_a_call_on_another_stream_belong_to_it():
     g = gen(17)
     kp, vp = ref.pools(40, 1, 48, BF, g)
     cache = PagedCache(16, 1, 48, 40, k_pages=kp, v_pages=vp)
-    table = ref.table_of([40], 40, g)
+    table = torch.full((1, 200), -1, dtype=torch.int32, device="cuda")   # wide: with a workspace
+    table[:, :40] = ref.table_of([40], 40, g)
     q = rand((2, 16, 48), BF, g)
     args = (q, table, ref.i32([0, 2]), ref.i32([0]), ref.i32([5001]))
     want = cache.attend(*args, causal=True)
@@ -453,6 +469,6 @@ def test_allocations_of_a_call_on_another_stream_belong_to_it():
     for _ in range(20):
         got.append(cache.attend(*args, causal=True, stream=side))
         for _ in range(3):
-            torch.full((cache.workspace_bytes(2, 1),), 255, dtype=torch.uint8, device="cuda")
+            torch.full((cache.workspace_bytes(2, 1, 200),), 255, dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for x in got)

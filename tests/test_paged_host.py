@@ -53,11 +53,12 @@ def test_null_arguments_and_a_host_only_cache():
     h = ctypes.c_void_p(5)
     assert L.bca_paged_create(None, ctypes.byref(h)) == _abi.BCA_ERR_INVALID_ARGUMENT and not h.value
     L.bca_paged_destroy(None)
-    assert L.bca_paged_pool_bytes(None) == 0 and L.bca_paged_workspace_bytes(None, 5, 5) == 0
+    assert L.bca_paged_pool_bytes(None) == 0 and L.bca_paged_workspace_bytes(None, 5, 5, 5) == 0
     assert L.bca_paged_status(None, None) == _abi.BCA_ERR_INVALID_ARGUMENT
     c = PagedCache(16, 2, 48, 10, layers=2, host_only=True)
     assert c.pool_bytes == 10 * 2 * PAGE * 48 * 2
-    assert c.workspace_bytes(0, 5) == 0 and c.workspace_bytes(5, 0) == 0 and c.workspace_bytes(5, 1) > 0
+    assert c.workspace_bytes(0, 5, 9) == 0 and c.workspace_bytes(5, 0, 9) == 0 and c.workspace_bytes(5, 1, -1) == 0
+    assert c.workspace_bytes(1, 1, 9) == 0 and c.workspace_bytes(1, 1, 9999) > 0 and c.workspace_bytes(500, 1, 9) > 0
     assert c.status() == _abi.BCA_ERR_HOST_ONLY_PLAN
     z = [None] * 3
     assert L.bca_paged_write(c._h, None, None, 0, *z, 0, 0, *[None] * 5) == _abi.BCA_ERR_HOST_ONLY_PLAN
