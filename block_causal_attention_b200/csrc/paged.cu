@@ -282,9 +282,16 @@ int launch_copy(const CopyArgs &a, const PagedCache &c, const int32_t *pairs, in
 // at a time: three trips to memory whatever their number up to 32, and two, four rows a warp,
 // for up to four.
 
-// Calls that a cluster an item takes: up to this many items, tables up to this wide.
-constexpr int kClusterItems = 32;
-constexpr int kClusterPages = 64;
+// Calls that go by clusters: 16-row tiles, few items, tables up to this wide.  Measured with one
+// query token, us by clusters / by shares, D = 24 and D = 48:
+//   items, tokens     1,000               8,000               16,000              32,000
+//    8             5.6/9.0  5.7/10.3   8.6/10.3  9.2/11.6  12/12  13/14        18/14  20/16
+//   16             6.0/9.2   11/11     9.2/12     17/14    13/15  24/17        20/20  40/23
+//   32              10/10    16/12      14/15     25/17    19/20  38/24        28/32  64/41
+// (At D = 48 a multiprocessor has registers for one block of a cluster, so 16 clusters do not run
+// at once.  32-row tiles gain at no size: 12.3/11.1 at 8 items of 1,000 tokens.)
+constexpr int kClusterPages = 96;
+int cluster_items(int d) { return d == 48 ? 8 : 16; }
 
 constexpr int kJoinThreads = 256;
 constexpr int kJoinFew = 4;  // pieces that are joined in one go
@@ -445,9 +452,9 @@ int by_type(const PagedCache &c, F &&f) {
 PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices, int width) {
     const int64_t group = c.hq / c.hkv, rows = nq * group / std::max(slices, 1);
     PagedShape s = {rows <= 16 ? 16 : rows <= 64 ? 32 : kPagedTileRows, 0};
-    if (s.rows < kPagedTileRows && nq <= kPagedShares && slices <= kPagedShares) {
+    if (s.rows == 16 && nq <= kPagedShares && slices <= kPagedShares) {
         const int64_t items = (nq * group + (int64_t)slices * (s.rows - 1)) / s.rows * c.hkv;
-        if (items <= kClusterItems && width <= kClusterPages) s.items = (int)items;
+        if (items <= cluster_items(c.d) && width <= kClusterPages) s.items = (int)items;
     }
     return s;
 }

@@ -398,16 +398,15 @@ ldsm_v<NV>(vs + vaddr, vf);
 
 template <int D, typename T>
 const void *rows_kernel(int rows, bool cluster) {
-    if (cluster)
-        return rows == 16 ? (const void *)paged_rows_kernel<D, T, 1, kCluster>
-                          : (const void *)paged_rows_kernel<D, T, 2, kCluster>;
+    if (cluster) return (const void *)paged_rows_kernel<D, T, 1, kCluster>;
     return rows == 16 ? (const void *)paged_rows_kernel<D, T, 1, 1> : (const void *)paged_rows_kernel<D, T, 2, 1>;
 }
 
 template <int D>
 const void *rows_kernel(bool f16, int rows, bool cluster, int &bytes) {
-    bytes = cluster ? (rows == 16 ? RowsSmem<D, 1, kCluster>::BYTES : RowsSmem<D, 2, kCluster>::BYTES)
-                    : (rows == 16 ? RowsSmem<D, 1, 1>::BYTES : RowsSmem<D, 2, 1>::BYTES);
+    bytes = cluster      ? RowsSmem<D, 1, kCluster>::BYTES
+            : rows == 16 ? RowsSmem<D, 1, 1>::BYTES
+                         : RowsSmem<D, 2, 1>::BYTES;
     return f16 ? rows_kernel<D, __half>(rows, cluster) : rows_kernel<D, __nv_bfloat16>(rows, cluster);
 }
 
@@ -425,6 +424,7 @@ const void *rows_kernel(const PagedCache &c, int rows, bool cluster, int &bytes)
 int prepare_paged_rows(const PagedCache &c) {
     for (int rows : {16, 32})
         for (bool cluster : {false, true}) {
+            if (cluster && rows != 16) continue;
             int bytes = 0;
             const void *f = rows_kernel(c, rows, cluster, bytes);
             if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
