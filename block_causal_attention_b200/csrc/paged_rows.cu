@@ -9,7 +9,9 @@
 // flight: one block a multiprocessor, a ring of whole pages (a page's keys and values of one
 // head are two contiguous stretches, moved by two bulk copies) filled by one warp that runs
 // ahead over page and item borders.  Eight warps take 16 of a page's 128 tokens each; their
-// results meet once an item, so that one page is enough work for all of them.
+// results meet once an item, so that one page is enough work for all of them.  Measured: one
+// token of 128 heads over 172,800 keys of 8 KV heads, D = 48, 49 us (5.4 TB/s with the launch and
+// the joining pass, about 8 us); 32 tokens over 512,000 keys 139 us, 5.9 TB/s.
 //
 // The layout of the pages is that of the 8 x 8 matrices that ldmatrix reads: 8 tokens x 8
 // channels of K and 8 channels x 8 tokens of V lie in 128 contiguous bytes, so both operands
@@ -34,7 +36,7 @@ constexpr int kWarpTokens = kPage / kWarps;   // 16
 template <int D, int MT, int CL>
 struct RowsSmem {
     static constexpr int TILE = D * kPage * 2;
-    // one block a multiprocessor with all of its shared memory; of a cluster's blocks two
+    // one block a multiprocessor with all of its shared memory; of a cluster's blocks two (D < 48)
     static constexpr int STAGES = CL == 1 ? (D == 48 ? 7 : D == 32 ? 10 : 13) : (D == 48 ? 3 : D == 32 ? 5 : 6);
     static constexpr int QSTRIDE = D == 24 ? 40 : D + 8;  // elements; an odd number of 16-byte units
     static constexpr int OFF_RING = 0;
