@@ -364,9 +364,9 @@ struct Io<__nv_bfloat16> {
     static constexpr bool kF16 = false;
     // P = 2^(s - reference) in bf16 has fp32's exponents: no shift is needed
     static constexpr float kShift = 0.f;
-    // sums of weights may reach this before the reference moves: far below fp32's 2^128, with
-    // room for the values and for 2^31 keys
-    static constexpr float kTop = 1.15292150460684698e18f;  // 2^60
+    // sums of weights may reach this before the reference moves: fp32's 2^128 leaves room for
+    // values up to 2^90 and a hundred thousand keys
+    static constexpr float kTop = 1048576.f;  // 2^20
     static __device__ __forceinline__ float2 unpack(uint32_t u) {
         return __bfloat1622float2(*reinterpret_cast<const __nv_bfloat162 *>(&u));
     }

@@ -412,7 +412,7 @@ int bca_paged_copy(bca_paged_t cache, const int32_t *pairs, int64_t n, void *k_p
  * of chunks is one slice per chunk, a KV range is the slice's k_begin, one new token of each
  * of B videos is B slices of one row.  The new tokens' own keys have been written before.
  *   q      : io type [nq][Hq][D];  o: the same, or fp32 with BCA_O_FP32
- *   pos    : device int32 [nq][3] or NULL: q is given post-prologue (q_gain NULL then)
+ *   pos    : device int32 [nq][3] or NULL: q is given post-prologue (|x| < 65504; q_gain NULL)
  *   off    : device int32 [slices + 1], non-decreasing;  seq: device int32 [slices], a value
  *            outside [0, seqs) is a slice that sees no key, or NULL: slice i reads row i;
  *   k_begin, k_end: device int32 [slices]

@@ -39,13 +39,14 @@ def unpage(k_pages, v_pages, row, tokens):
     return k[:tokens], v[:tokens]
 
 
-def attend(q, k_pages, v_pages, table, off, seq, k_begin, k_end, causal, pos=None, gain=None):
+def attend(q, k_pages, v_pages, table, off, seq, k_begin, k_end, causal, pos=None, gain=None,
+           base=(1e4, 1e4, 1e4)):
     """(O, LSE [Hq, nq], error bound of O, error bound of LSE), row by row over the keys that
     are there.  The bounds count, to first order with a tenth on top: q_hat rounded to fp16
     (2^-11 of each product of a score), P rounded to the values' type, O rounded once, and
     2^-18 for the fp32 steps (a dozen of 2^-24, ex2 2^-22, products of up to 48 terms)."""
     t = q.dtype
-    qh = prologue(q, pos, gain)
+    qh = prologue(q, pos, gain, base)
     nq, hq, d = q.shape
     hkv = k_pages.shape[1]
     grp = hq // hkv

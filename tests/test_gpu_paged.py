@@ -472,3 +472,127 @@ def test_allocations_of_a_call_on_another_stream_belong_to_it():
             torch.full((cache.workspace_bytes(2, 1, 200),), 255, dtype=torch.uint8, device="cuda")
     torch.cuda.synchronize()
     assert all(torch.equal(x, want) for x in got)
+
+
+@pytest.mark.parametrize("hq,hkv,new", [(400, 1, [1, 3]), (130, 2, [1, 1, 2]), (9, 9, [40, 3]), (20, 20, [1] * 9)])
+def test_attend_odd_groups_and_head_counts(hq, hkv, new):
+    check_attend(hq, hkv, 24, BF, new, [300 + 7 * i for i in range(len(new))], True, True, 18)
+
+
+@pytest.mark.parametrize("d", [24, 32, 48])
+def test_any_positions_and_bases(d):
+    """Negative and far positions, bases below, at and above 1: the angle is that of the 64-bit
+    product (off by at most 2^31 * 2^-53 of its own turns in the reference, 2 pi 2^-22 rad)."""
+    g = gen(19)
+    # the ABI takes bases in fp32, so the reference has to start from fp32's 0.7 too: at 2^31 their
+    # difference, 1.2e-8, is a hundred thousand turns
+    base = tuple(torch.tensor(x, dtype=torch.float32).item() for x in (0.7, 1.0, 3e5))
+    edge = torch.tensor([0, 1, -1, 12345678, -87654321, 2 ** 31 - 1, -2 ** 31], device="cuda", dtype=torch.int32)
+    pos = edge[torch.randint(0, 7, (60, 3), generator=g, device="cuda")].contiguous()
+    kp, vp = ref.pools(2, 2, d, BF, g)
+    cache = PagedCache(4, 2, d, 2, rope_base=base, k_pages=kp, v_pages=vp)
+    k, v, q = rand((60, 2, d), BF, g), rand((60, 2, d), BF, g), rand((60, 4, d), BF, g)
+    table = ref.i32([[1]])
+    cache.write(k, v, table, ref.i32([0, 60]), ref.i32([30]), pos=pos)
+    got, _ = ref.unpage(kp[0], vp[0], [1], 90)
+    want = ref.prologue(k, pos, None, base)
+    # base 0.7: angles grow with the pair, up to 2^31 * 0.7^(-7/8) turns / 2 pi
+    bound = 2.0 ** -11 * want.abs() + 2.0 ** -25 + 2.0 ** -18 * want.abs().amax(2, keepdim=True)
+    no_worse(got[30:], want, bound, "k")
+    o = cache.attend(q, table, ref.i32([0, 60]), ref.i32([30]), ref.i32([90]), pos=pos)
+    assert cache.status() == _abi.BCA_OK
+    wo, _, bo, _ = ref.attend(q, kp[0], vp[0], table, [0, 60], [0], [30], [90], False, pos, None, base)
+    # the queries' angles: 2^-20 of a value more (cos and sin to 2^-20.5 each), in every product of a score
+    no_worse(o, wo, bo + 2.0 ** -16, "o")
+
+
+def test_large_values_survive_a_moving_reference():
+    """Values near 2^90 while the scores rise by a hundred: no sum may overflow on the way."""
+    g = gen(20)
+    d = 32
+    kp, vp = ref.pools(12, 1, d, BF, g)
+    vp *= 2.0 ** 90
+    table = ref.table_of([12], 12, g)
+    for i, p in enumerate(table[0].tolist()):
+        kp[0, p] *= 0.5 + 2 * i
+    cache = PagedCache(8, 1, d, 12, k_pages=kp, v_pages=vp)
+    for n in (1, 5, 60):
+        q = rand((n, 8, d), BF, g)
+        o = cache.attend(q, table, ref.i32([0, n]), ref.i32([0]), ref.i32([1500]), causal=True)
+        assert cache.status() == _abi.BCA_OK
+        wo, _, bo, _ = ref.attend(q, kp[0], vp[0], table, [0, n], [0], [0], [1500], True)
+        assert wo.isfinite().all()
+        no_worse(o, wo, bo, "o")
+
+
+def test_tables_without_rows_or_columns():
+    g = gen(21)
+    cache = PagedCache(4, 2, 48, 3)
+    for shape in ((0, 5), (2, 0), (0, 0)):
+        table = torch.zeros(shape, dtype=torch.int32, device="cuda")
+        for n in (1, 40, 300):
+            q, k = rand((2 * n, 4, 48), BF, g), rand((2 * n, 2, 48), BF, g)
+            lse = torch.zeros((4, 2 * n), device="cuda")
+            o = cache.attend(q, table, ref.i32([0, n, 2 * n]), ref.i32([0, 0]), ref.i32([10, 0]), seq=ref.i32([0, 1]), lse=lse)
+            assert (o == 0).all() and (lse == -math.inf).all()
+            cache.write(k, k, table, ref.i32([0, n, 2 * n][:shape[0] + 1]), ref.i32([0] * shape[0]))
+            assert cache.status() == (_abi.BCA_ERR_BAD_PAGE if shape[0] else _abi.BCA_OK)
+    assert cache.attend(rand((3, 4, 48), BF, g), table, ref.i32([0]), ref.i32([]), ref.i32([]), seq=ref.i32([])).shape[0] == 3
+
+
+def test_pools_beyond_32_bits():
+    """Page numbers whose bytes and elements pass 2^32: the last pages of a pool of 10 GB."""
+    g = gen(22)
+    hkv, d, pages, layers = 8, 48, 26000, 2
+    cache = PagedCache(16, hkv, d, pages, layers=layers)
+    assert cache.pool_bytes * layers > 2 ** 32
+    row = [pages - 1, pages - 3, 5]
+    table, n = ref.i32([row]), 300
+    k, v, q = rand((n, hkv, d), BF, g), rand((n, hkv, d), BF, g), rand((2, 16, d), BF, g)
+    cache.write(k, v, table, ref.i32([0, n]), ref.i32([0]), layer=1)
+    got_k, got_v = ref.unpage(cache.k_pages[1], cache.v_pages[1], row, n)
+    assert torch.equal(got_k, k.half().double()) and torch.equal(got_v, v.double())
+    cache.copy_pages([[pages - 1, 7], [pages - 3, pages - 2]])
+    moved = [7, pages - 2, 5]
+    for r in (row, moved):
+        o = cache.attend(q, ref.i32([r]), ref.i32([0, 2]), ref.i32([0]), ref.i32([n]), causal=True, layer=1)
+        assert cache.status() == _abi.BCA_OK
+        wo, _, bo, _ = ref.attend(q, cache.k_pages[1], cache.v_pages[1], ref.i32([r]), [0, 2], [0], [0], [n], True)
+        no_worse(o, wo, bo, "o")
+
+
+def test_copies_of_thousands_of_pages_and_in_a_graph():
+    g = gen(23)
+    moves = 4500
+    kp, vp = ref.pools(2 * moves, 1, 24, BF, g)
+    cache = PagedCache(1, 1, 24, 2 * moves, k_pages=kp, v_pages=vp)
+    order = torch.randperm(2 * moves, generator=g, device="cuda")
+    src, dst = order[:moves], order[moves:]
+    wk, wv = kp.clone(), vp.clone()
+    wk[:, dst], wv[:, dst] = kp[:, src], vp[:, src]
+    pairs = torch.stack([src, dst], 1).cpu()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.copy_pages(pairs)
+    pairs.zero_()                                # read before the call returned
+    graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(kp, wk) and torch.equal(vp, wv)
+
+
+def test_calls_on_two_streams_at_once():
+    g = gen(24)
+    kp, vp = ref.pools(80, 2, 48, BF, g)
+    cache = PagedCache(16, 2, 48, 80, k_pages=kp, v_pages=vp)
+    table = widened(ref.table_of([40, 40], 80, g))
+    calls = []
+    for n in (1, 4, 500):
+        q = rand((2 * n, 16, 48), BF, g)
+        calls.append((q, table, ref.i32([0, n, 2 * n]), ref.i32([3, 0]), ref.i32([5001, 4700])))
+    want = [cache.attend(*c, causal=True) for c in calls]
+    streams = [torch.cuda.Stream() for _ in calls]
+    torch.cuda.synchronize()
+    got = [[cache.attend(*c, causal=True, stream=s) for c, s in zip(calls, streams)] for _ in range(10)]
+    torch.cuda.synchronize()
+    assert cache.status() == _abi.BCA_OK
+    assert all(torch.equal(x, w) for r in got for x, w in zip(r, want))
