@@ -224,40 +224,53 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
                 for (int k = 0; k < KS; ++k) ldsm4(ks + kaddr + k * (2 * kPage * 16), kf[k]);
                 if constexpr (TAIL)
                     ldsm2(ks + KS * (2 * kPage * 16) + (2 * warp + (lane >> 3 & 1)) * 128 + (lane & 7) * 16, kt[0], kt[1]);
-ldsm_v<NV>(vs + vaddr, vf);
+                ldsm_v<NV>(vs + vaddr, vf);
 
                 const bool inside = key0 >= kb && key0 + kWarpTokens <= lim_all;
                 bool odd = false;  // values that are not finite, at keys that some rows do not see
                 if (!inside) odd = clear_unseen<T, NV>(vf, key0 + 2 * t, kb, lim_any);
+                // each step for all row tiles before the next one: their chains run side by side
+                float s[MT][2][4] = {}, mx[MT][2];
 #pragma unroll
-                for (int m = 0; m < MT; ++m) {
-                    float s[2][4] = {};
+                for (int k = 0; k < KS; ++k)
 #pragma unroll
-                    for (int k = 0; k < KS; ++k) {
-                        mma16<true>(s[0], qa[m][k], kf[k][0], kf[k][1]);
-                        mma16<true>(s[1], qa[m][k], kf[k][2], kf[k][3]);
+                    for (int m = 0; m < MT; ++m) {
+                        mma16<true>(s[m][0], qa[m][k], kf[k][0], kf[k][1]);
+                        mma16<true>(s[m][1], qa[m][k], kf[k][2], kf[k][3]);
                     }
-                    if constexpr (TAIL) {
-                        mma8_f16(s[0], qt[m][0], qt[m][1], kt[0]);
-                        mma8_f16(s[1], qt[m][0], qt[m][1], kt[1]);
+                if constexpr (TAIL) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        mma8_f16(s[m][0], qt[m][0], qt[m][1], kt[0]);
+                        mma8_f16(s[m][1], qt[m][0], qt[m][1], kt[1]);
                     }
-                    if (!inside) {
+                }
+                if (!inside) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
 #pragma unroll
                         for (int n = 0; n < 2; ++n)
 #pragma unroll
                             for (int j = 0; j < 4; ++j) {
                                 const int32_t key = key0 + 8 * n + 2 * t + (j & 1);
-                                if (key < kb || key >= lim[m][j >> 1]) s[n][j] = -INFINITY;
+                                if (key < kb || key >= lim[m][j >> 1]) s[m][n][j] = -INFINITY;
                             }
+                }
+                bool grow = false;
+#pragma unroll
+                for (int m = 0; m < MT; ++m)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        mx[m][h] = fmaxf(fmaxf(s[m][0][2 * h], s[m][0][2 * h + 1]),
+                                         fmaxf(s[m][1][2 * h], s[m][1][2 * h + 1])) * a.scale;
+                        grow |= mx[m][h] > ref[m][h] + (kShift + kLazy);
                     }
-                    float mx[2];
-                    mx[0] = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1])) * a.scale;
-                    mx[1] = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3])) * a.scale;
-                    const bool grow = mx[0] > ref[m][0] + (kShift + kLazy) || mx[1] > ref[m][1] + (kShift + kLazy);
-                    if (__any_sync(0xffffffffu, grow)) {
+                if (__any_sync(0xffffffffu, grow)) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
 #pragma unroll
                         for (int h = 0; h < 2; ++h) {
-                            float top = mx[h];
+                            float top = mx[m][h];
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
                             if (top > ref[m][h] + (kShift + kLazy)) {
@@ -272,23 +285,29 @@ ldsm_v<NV>(vs + vaddr, vf);
                                 }
                             }
                         }
-                    }
-                    const float sub[2] = {ref[m][0] == -INFINITY ? 0.f : ref[m][0],
-                                          ref[m][1] == -INFINITY ? 0.f : ref[m][1]};
+                }
+                uint32_t pa[MT][4];  // P in the values' type: it is a factor of the matrix product
 #pragma unroll
-                    for (int n = 0; n < 2; ++n)
+                for (int m = 0; m < MT; ++m)
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            s[n][j] = ex2(fmaf(s[n][j], a.scale, -sub[j >> 1]));
-                            sum[m][j >> 1] += s[n][j];
+                    for (int h = 0; h < 2; ++h) {
+                        const float neg = ref[m][h] == -INFINITY ? 0.f : -ref[m][h];
+#pragma unroll
+                        for (int n = 0; n < 2; ++n) {
+                            const float y0 = ex2(fmaf(s[m][n][2 * h], a.scale, neg));
+                            const float y1 = ex2(fmaf(s[m][n][2 * h + 1], a.scale, neg));
+                            sum[m][h] += y0 + y1;
+                            pa[m][2 * n + h] = Io<T>::pack(y0, y1);
                         }
-                    // P in the values' type: it is a factor of the matrix product
-                    const uint32_t pa[4] = {Io<T>::pack(s[0][0], s[0][1]), Io<T>::pack(s[0][2], s[0][3]),
-                                            Io<T>::pack(s[1][0], s[1][1]), Io<T>::pack(s[1][2], s[1][3])};
+                    }
 #pragma unroll
-                    for (int n = 0; n < NV; ++n) mma16<Io<T>::kF16>(o[m][n], pa, vf[n][0], vf[n][1]);
-                    if (odd)
-                        add_left_out<D, T, NV>(o[m], pa,
+                for (int n = 0; n < NV; ++n)
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) mma16<Io<T>::kF16>(o[m][n], pa[m], vf[n][0], vf[n][1]);
+                if (odd) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m)
+                        add_left_out<D, T, NV>(o[m], pa[m],
                                                reinterpret_cast<const T *>(smem + (vs - sbase)) + 2 * warp * D * 8, key0,
                                                kb, lim[m]);
                 }
