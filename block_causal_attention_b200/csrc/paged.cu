@@ -307,7 +307,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) paged_join_kernel(const __gri
     if (j.last < c) return;
     // The workspace is the caller's.  Two calls that overlap with one workspace may read each
     // other's notes: their results are lost, but nothing outside their arrays is touched.
-    if (j.last >= kPagedShares || (uint32_t)j.g >= (uint32_t)a.hkv || (uint32_t)j.head >= (uint32_t)a.group ||
+    if (j.last >= paged_shares(a.rows) || (uint32_t)j.g >= (uint32_t)a.hkv || (uint32_t)j.head >= (uint32_t)a.group ||
         j.left > a.rows) {
         if (threadIdx.x == 0) atomicOr(a.status, kPagedWorkspace);
         return;
@@ -419,7 +419,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) paged_join_kernel(const __gri
 template <int D, typename T>
 int launch_join(const PagedArgs &a, cudaStream_t stream) {
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)kPagedShares, (unsigned)(a.rows < kPagedTileRows ? a.rows / 8 : 12));
+    cfg.gridDim = dim3((unsigned)paged_shares(a.rows), (unsigned)(a.rows <= 32 ? a.rows / 8 : a.rows / 32));
     cfg.blockDim = dim3(kJoinThreads);
     cfg.stream = stream;
     cudaLaunchAttribute attr = {};
@@ -445,16 +445,20 @@ int by_type(const PagedCache &c, F &&f) {
 
 }  // namespace
 
-// Tiles of 16, 32 or 384 packed rows, by the rows of an average slice (the sizes of single ones
-// are device data).  Measured on 16 sequences of 8,000 tokens and 8 KV heads, D = 24 / 48, us:
-//   rows of a slice       16          32          64          128         256
-//   16-row tiles        33 / 40     57 / 67    106 / 118   203 / 220   397 / 431
-//   32-row tiles        47 / 54     48 / 55     86 / 97    164 / 182   316 / 350
-//   384-row tiles       89 / 111    90 / 112    91 / 114    92 / 116   123 / 155
+// Tiles of 16, 32, 128 or 384 packed rows, by the rows of an average slice (the sizes of single
+// ones are device data).  Measured on 16 sequences of 8,000 tokens and 8 KV heads and on one of
+// 20,000, D = 24 / 48, us:
+//   rows of a slice       16         32         64         128        256        512       1 x 64    1 x 384
+//   16-row tiles        32 / 39    57 / 68   109 / 123  212 / 237  416 / 464  826 / 927   26 / 30  102 / 110
+//   32-row tiles        39 / 45    40 / 47    73 / 82   138 / 152  266 / 290  523 / 571   20 / 23   65 / 70
+//   128-row tiles       68 / 78    69 / 80    69 / 81    71 / 83   121 / 136  222 / 253   33 / 41   47 / 57
+//   384-row tiles       90 / 110   90 / 111   90 / 112   92 / 114  121 / 154  227 / 286   36 / 45   52 / 72
+// and on chunks, 128- against 384-row tiles: the 4.5B window 1,016 / 876 us, half a 720p chunk
+// 2,270 / 2,220, ragged chunks of several streams 408 / 322.
 PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices, int width) {
     const int64_t group = c.hq / c.hkv, rows = nq * group / std::max(slices, 1);
-    PagedShape s = {rows <= 16 ? 16 : rows <= 64 ? 32 : kPagedTileRows, 0};
-    if (s.rows == 16 && nq <= kPagedShares && slices <= kPagedShares) {
+    PagedShape s = {rows <= 16 ? 16 : rows <= 64 ? 32 : rows <= 256 ? kPagedNarrowRows : kPagedTileRows, 0};
+    if (s.rows == 16 && nq <= 1024 && slices <= 1024) {
         const int64_t items = (nq * group + (int64_t)slices * (s.rows - 1)) / s.rows * c.hkv;
         if (items <= cluster_items(c.d) && width <= kClusterPages) s.items = (int)items;
     }
@@ -463,7 +467,7 @@ PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices, int width) {
 
 size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices, int width) {
     const PagedShape s = paged_shape(c, nq, slices, width);
-    return s.items > 0 ? 0 : kPagedShares * (kPagedJoinBytes + 2 * (size_t)s.rows * (c.d + 2) * sizeof(float));
+    return s.items > 0 ? 0 : paged_shares(s.rows) * (kPagedJoinBytes + 2 * (size_t)s.rows * (c.d + 2) * sizeof(float));
 }
 
 int prepare_paged(const PagedCache &c) {
@@ -531,6 +535,7 @@ int launch_paged_copy(const PagedCache &c, const int32_t *pairs, int64_t n, void
 }
 
 int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream_t stream) {
+    const PagedShape s = paged_shape(c, io.nq, io.slices, io.width);
     PagedArgs a;
     a.q = io.q;
     a.pos = io.pos;
@@ -545,7 +550,7 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
     a.o = io.o;
     a.lse = io.lse;
     a.joins = static_cast<PagedJoin *>(io.workspace);
-    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(io.workspace) + (size_t)kPagedShares * kPagedJoinBytes);
+    a.part = reinterpret_cast<float *>(static_cast<uint8_t *>(io.workspace) + (size_t)paged_shares(s.rows) * kPagedJoinBytes);
     a.status = c.d_status;
     a.nq = io.nq;
     a.pages = c.pages;
@@ -556,7 +561,6 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
     a.hq = c.hq;
     a.hkv = c.hkv;
     a.group = c.hq / c.hkv;
-    const PagedShape s = paged_shape(c, io.nq, io.slices, io.width);
     a.rows = s.rows;
     a.o_fp32 = (c.flags & BCA_O_FP32) ? 1 : 0;
     a.eps = c.eps;
@@ -571,7 +575,7 @@ int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream
     while (a.shift < 27 && items * (64.0 + std::ldexp(keys, -4 - a.shift)) > 2e9) ++a.shift;
     if (items * 65.0 > 2e9) return BCA_ERR_TOO_LARGE;
     const int rc =
-        a.rows == kPagedTileRows ? launch_paged_tiles(c, a, stream) : launch_paged_rows(c, a, s.items, stream);
+        a.rows >= kPagedNarrowRows ? launch_paged_tiles(c, a, stream) : launch_paged_rows(c, a, s.items, stream);
     if (rc != BCA_OK || s.items > 0) return rc;
     return by_type(c, [&](auto d, auto t) { return launch_join<decltype(d)::value, decltype(t)>(a, stream); });
 }

@@ -11,9 +11,11 @@
 namespace bca {
 
 constexpr int kPage = BCA_PAGE_TOKENS;
-constexpr int kPagedShares = 148;    // blocks of an attention call: one a multiprocessor
 constexpr int kPagedJoinBytes = 32;  // of the workspace, for each share
 constexpr int kPagedTileRows = 384;  // packed rows of a work item of paged_tiles.cu
+constexpr int kPagedNarrowRows = 128;  // and of its form for slices of few
+// Blocks of an attention call with tiles of so many rows: all that run at once.
+constexpr int paged_shares(int rows) { return rows == kPagedNarrowRows ? 296 : 148; }
 
 // status-word bits written by the paged kernels
 constexpr int kPagedTimeout = 0x1;

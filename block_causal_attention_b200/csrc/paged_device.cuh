@@ -46,8 +46,8 @@ struct PagedArgs {
 // A slice's queries are packed token by token, the `group` query heads of a KV head next to
 // one another, and cut into tiles of `rows` packed rows: the rows of a tile read the same
 // keys.  An item is a tile of one KV head.  Items stand in a row (slice, KV head, tile), each
-// as long as its weight, about the keys it reads; block c takes the c-th of kPagedShares
-// equal stretches of that row.  A stretch that ends inside an item splits the item's pages in
+// as long as its weight, about the keys it reads; block c takes the c-th of as many
+// equal stretches as there are blocks of that row.  A stretch that ends inside an item splits the item's pages in
 // proportion; the pieces are joined by paged_join_kernel.  So the load is even whatever the
 // lengths are (they are device data), and the cut depends on the arguments alone: the same
 // call gives the same bits.
@@ -55,13 +55,13 @@ struct PagedArgs {
 // Weight of an item that reads no page, in units of 16 << shift keys: its prologue, its epilogue
 // and its first page, as measured: one page of the register tiles, two pages of the 384-row
 // tiles, four with the causal rule, whose last pages are masked (fitted to the blocks' clocks:
-// 8,500 and 17,200 cycles an item beside 4,200 a page).  The whole row of items is below 2^31
+// 8,500 and 17,200 cycles an item beside 4,200 a page; a page of the 128-row tiles takes less).  The whole row of items is below 2^31
 // units long (the host picks the shift for the sizes of the call), so all of this is 32-bit
 // arithmetic: before a block knows what to load it can do nothing else, and 64-bit divisions
 // here took 2 us.
 template <int R>
 __device__ __forceinline__ uint32_t paged_item_weight(bool causal) {
-    return R < kPagedTileRows ? 8u : causal ? 32u : 16u;
+    return R < kPagedNarrowRows ? 8u : R == kPagedNarrowRows ? (causal ? 40u : 24u) : causal ? 32u : 16u;
 }
 
 struct PagedSlice {
@@ -122,9 +122,10 @@ __device__ __forceinline__ int32_t paged_limit(const PagedArgs &a, const PagedSl
     return min(s.ke, s.end - (s.n - 1 - token));  // no overflow: both are >= 0 and below 2^31
 }
 
-// Where share c begins in a row of this total weight: total * c / kPagedShares.
+// Where share c begins in a row of this total weight: total * c / shares.
+template <int R>
 __device__ __forceinline__ uint32_t paged_share(uint32_t total, int c) {
-    constexpr uint32_t n = kPagedShares;
+    constexpr uint32_t n = paged_shares(R);
     const uint32_t x = (uint32_t)c;
     return total / n * x + total % n * x / n;
 }
@@ -197,8 +198,8 @@ __device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, uint32_t
         sum += mine;
     }
     total = __reduce_add_sync(0xffffffffu, sum);
-    lo = paged_share(total, c);
-    hi = paged_share(total, c + 1);
+    lo = paged_share<R>(total, c);
+    hi = paged_share<R>(total, c + 1);
     if (lo == hi) return false;
 
     // (offsets that do not rise may make the whole longer than 2^32, and then nothing be found)
@@ -343,9 +344,9 @@ __device__ __forceinline__ void paged_join_of(const PagedArgs &a, const PagedCur
     else if (cur.end() > hi) {
         // the last share that begins before the item ends: an estimate, put right
         const uint32_t end = cur.end();
-        int k = min((int)((float)end / (float)total * kPagedShares), kPagedShares - 1);
-        while (k > c && paged_share(total, k) >= end) --k;
-        while (k + 1 < kPagedShares && paged_share(total, k + 1) < end) ++k;
+        int k = min((int)((float)end / (float)total * paged_shares(R)), paged_shares(R) - 1);
+        while (k > c && paged_share<R>(total, k) >= end) --k;
+        while (k + 1 < paged_shares(R) && paged_share<R>(total, k + 1) < end) ++k;
         j.last = k;
     }
     a.joins[c] = j;
@@ -531,7 +532,7 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
     // An item is published when the ring's worth of pages of the one before it is on the way, so
     // that no page waits for it; for the 384-row tiles before those pages, since two warps need the
     // time of four pages for its queries (ragged chunks: 341 us the other way, 318 us).
-    constexpr bool kEarly = R == kPagedTileRows;
+    constexpr bool kEarly = R >= kPagedNarrowRows;
     int published = 0;
     PagedItem x;
     const int32_t *row = nullptr;

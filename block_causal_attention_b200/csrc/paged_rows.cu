@@ -460,7 +460,7 @@ int launch_paged_rows(const PagedCache &c, const PagedArgs &a, int items, cudaSt
     PagedArgs args = a;
     void *params[] = {&args};
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(items > 0 ? items * kCluster : kPagedShares));
+    cfg.gridDim = dim3((unsigned)(items > 0 ? items * kCluster : paged_shares(a.rows)));
     cfg.blockDim = dim3(kThreads);
     cfg.dynamicSmemBytes = (size_t)bytes;
     cfg.stream = stream;

@@ -32,30 +32,30 @@ using namespace sm100;
 
 namespace {
 
-constexpr int kSlots = 3;                  // 128-row tiles that share a page
-constexpr int kBuffers = 4;                // S tiles of 128 x 128 in tensor memory, used in turn
-constexpr int kRows = kPagedTileRows;
-constexpr int kThreads = 128 + 128 * kSlots;
-static_assert(kRows == 128 * kSlots, "rows of a work item");
-
-template <int D>
+// SL: 128-row tiles that share a page.  Three make a block that fills a multiprocessor; with one,
+// for slices of 65 to 256 rows, two blocks share it (a block of three with one tile at work had a
+// softmax warp a scheduler: 114 against 83 us for 16 sequences of 8,000 tokens, 128 rows each).
+template <int D, int SL>
 struct TilesSmem {
+    static constexpr int ROWS = 128 * SL;
+    static constexpr int BUFFERS = SL == 1 ? 2 : 4;  // S tiles of 128 x 128 in tensor memory, used in turn
+    static constexpr int THREADS = 128 + 128 * SL;
     static constexpr int DPAD = Geo<D>::DPAD;
     static constexpr int TILE = D * kPage * 2;       // bytes of a page's K or V of one head
     static constexpr int KSTAGE = DPAD * kPage * 2;  // K is padded to whole 16-channel steps
     static constexpr int STAGE = KSTAGE + TILE;
-    static constexpr int STAGES = D == 48 ? 6 : 8;
+    static constexpr int STAGES = SL == 1 ? (D == 48 ? 3 : 5) : (D == 48 ? 6 : 8);
     static constexpr int Q_BYTES = 128 * DPAD * 2;
     static constexpr int OFF_Q = 0;
-    static constexpr int Q_ITEM = kSlots * Q_BYTES;
+    static constexpr int Q_ITEM = SL * Q_BYTES;
     static constexpr int OFF_RING = 2 * Q_ITEM;      // queries of this item and of the next
     static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE;
     static constexpr int B_FULL = 0;
     static constexpr int B_EMPTY = STAGES;
     static constexpr int B_ITEM = 2 * STAGES;
     static constexpr int B_S_FULL = B_ITEM + 2 * kItemRing;
-    static constexpr int B_S_FREE = B_S_FULL + kSlots * kBuffers;  // full: of a slot's use of a buffer
-    static constexpr int B_Q_FULL = B_S_FREE + kBuffers;
+    static constexpr int B_S_FREE = B_S_FULL + SL * BUFFERS;  // full: of a slot's use of a buffer
+    static constexpr int B_Q_FULL = B_S_FREE + BUFFERS;
     static constexpr int B_Q_FREE = B_Q_FULL + 2;
     static constexpr int B_Q_FIRST = B_Q_FREE + 2;
     static constexpr int B_DONE = B_Q_FIRST + 1;
@@ -63,7 +63,7 @@ struct TilesSmem {
     static constexpr int OFF_TMEM = OFF_HERE + 4 * STAGES;
     static constexpr int OFF_ITEMS = OFF_TMEM + 4;
     static constexpr int OFF_LIMIT = OFF_ITEMS + kItemRing * (int)sizeof(PagedItem);  // of each row
-    static constexpr int OFF_ABORT = OFF_LIMIT + 4 * kRows;
+    static constexpr int OFF_ABORT = OFF_LIMIT + 4 * ROWS;
     static constexpr int BYTES = OFF_ABORT + 4;
 };
 
@@ -90,6 +90,7 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&f)[4][4]) {
 template <int D, typename T>
 __device__ __forceinline__ void query_rows(const PagedArgs &a, const PagedItem &x, const float2 (&gain)[Row8<D>::N],
                                            uint8_t *to, int first) {
+    constexpr int kTile = TilesSmem<D, 1>::Q_BYTES;
     const int e = threadIdx.x & 7, r0 = first + (threadIdx.x >> 3 & 3);
     Row8<D> q[4];
 #pragma unroll
@@ -107,15 +108,17 @@ __device__ __forceinline__ void query_rows(const PagedArgs &a, const PagedItem &
         for (int k = 0; k < Row8<D>::N; ++k) {
             const int pr = e + 8 * k;
             if (pr < D / 2)
-                *reinterpret_cast<uint32_t *>(to + r / 128 * TilesSmem<D>::Q_BYTES + (pr >> 2) * 2048 + r % 128 * 16 +
+                *reinterpret_cast<uint32_t *>(to + r / 128 * kTile + (pr >> 2) * 2048 + r % 128 * 16 +
                                               (pr & 3) * 4) = r < x.left ? pack_f16x2(q[i].x[k].x, q[i].x[k].y) : 0u;
         }
     }
 }
 
-template <int D, typename T>
-__global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_constant__ PagedArgs a) {
-    using L = TilesSmem<D>;
+template <int D, typename T, int SL>
+__global__ void __launch_bounds__(TilesSmem<D, SL>::THREADS, SL == 1 ? 2 : 1)
+    paged_tiles_kernel(const __grid_constant__ PagedArgs a) {
+    using L = TilesSmem<D, SL>;
+    constexpr int kSlots = SL, kBuffers = L::BUFFERS, kRows = L::ROWS, kThreads = L::THREADS;
     constexpr int S = L::STAGES;
     constexpr int NV = D / 8;
     constexpr uint32_t IDESC = idesc_f32acc(128, 128, kFmtF16);
@@ -164,7 +167,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
     }
     fence_proxy_async_smem();
     if (warp == 2) {
-        tmem_alloc(smem_u32(tmem_ptr), 512);
+        tmem_alloc(smem_u32(tmem_ptr), 128 * kBuffers);
         tmem_relinquish();
     }
     tc_fence_before();
@@ -172,8 +175,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
     tc_fence_after();
     const uint32_t tbase = *tmem_ptr;
 
-    // Registers: 512 threads x 128 at launch; the softmax warps take 152 (48 sums of O and 32
-    // scores among them): 128 x 56 + 384 x 152 = 65,536.
+    // Registers: threads x 128 at launch; the softmax warps take 152 (48 sums of O and 32 scores
+    // among them), 128 x 56 + 384 x 152 = 512 x 128, or 200, 128 x 56 + 128 x 200 = 256 x 128.
     if (warp < 4) regs_dec<56>();
     if (warp == 0) {
         paged_fill<kRows, S, L::TILE, L::KSTAGE, L::STAGE>(a, c, sbase + L::OFF_RING, bar(L::B_FULL),
@@ -273,7 +276,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
         }
         __syncwarp();
     } else {
-        regs_inc<152>();
+        regs_inc<SL == 1 ? 200 : 152>();
         // ------------------------------------------------ softmax and O += P V
         const int slot = (warp - 4) >> 2, quarter = warp & 3;
         const int g = lane >> 2, t = lane & 3;
@@ -634,40 +637,46 @@ __global__ void __launch_bounds__(kThreads, 1) paged_tiles_kernel(const __grid_c
     __syncthreads();
     if (warp == 2) {
         tc_fence_after();
-        tmem_dealloc(tbase, 512);
+        tmem_dealloc(tbase, 128 * kBuffers);
     }
 }
 
-const void *tiles_kernel(const PagedCache &c, int &bytes) {
-    const bool f16 = (c.flags & BCA_PAGED_FP16) != 0;
+template <int D>
+const void *tiles_kernel(bool f16, bool narrow, int &bytes) {
+    bytes = narrow ? TilesSmem<D, 1>::BYTES : TilesSmem<D, 3>::BYTES;
+    if (narrow)
+        return f16 ? (const void *)paged_tiles_kernel<D, __half, 1> : (const void *)paged_tiles_kernel<D, __nv_bfloat16, 1>;
+    return f16 ? (const void *)paged_tiles_kernel<D, __half, 3> : (const void *)paged_tiles_kernel<D, __nv_bfloat16, 3>;
+}
+
+const void *tiles_kernel(const PagedCache &c, int rows, int &bytes) {
+    const bool f16 = (c.flags & BCA_PAGED_FP16) != 0, narrow = rows == kPagedNarrowRows;
     switch (c.d) {
-        case 24:
-            bytes = TilesSmem<24>::BYTES;
-            return f16 ? (const void *)paged_tiles_kernel<24, __half> : (const void *)paged_tiles_kernel<24, __nv_bfloat16>;
-        case 32:
-            bytes = TilesSmem<32>::BYTES;
-            return f16 ? (const void *)paged_tiles_kernel<32, __half> : (const void *)paged_tiles_kernel<32, __nv_bfloat16>;
-        default:
-            bytes = TilesSmem<48>::BYTES;
-            return f16 ? (const void *)paged_tiles_kernel<48, __half> : (const void *)paged_tiles_kernel<48, __nv_bfloat16>;
+        case 24: return tiles_kernel<24>(f16, narrow, bytes);
+        case 32: return tiles_kernel<32>(f16, narrow, bytes);
+        default: return tiles_kernel<48>(f16, narrow, bytes);
     }
 }
 
 }  // namespace
 
 int prepare_paged_tiles(const PagedCache &c) {
-    int bytes = 0;
-    const void *f = tiles_kernel(c, bytes);
-    return cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) == cudaSuccess ? BCA_OK
-                                                                                                      : BCA_ERR_CUDA;
+    for (int rows : {kPagedNarrowRows, kPagedTileRows}) {
+        int bytes = 0;
+        const void *f = tiles_kernel(c, rows, bytes);
+        if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+            return BCA_ERR_CUDA;
+    }
+    return BCA_OK;
 }
 
 int launch_paged_tiles(const PagedCache &c, const PagedArgs &a, cudaStream_t stream) {
     int bytes = 0;
-    const void *f = tiles_kernel(c, bytes);
+    const void *f = tiles_kernel(c, a.rows, bytes);
     PagedArgs args = a;
     void *params[] = {&args};
-    return cudaLaunchKernel(f, dim3((unsigned)kPagedShares), dim3(kThreads), params, (size_t)bytes, stream) == cudaSuccess
+    return cudaLaunchKernel(f, dim3((unsigned)paged_shares(a.rows)), dim3((unsigned)(128 + a.rows)), params,
+                            (size_t)bytes, stream) == cudaSuccess
                ? BCA_OK
                : BCA_ERR_CUDA;
 }
