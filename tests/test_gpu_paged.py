@@ -289,7 +289,7 @@ def test_attend_any_offsets_stay_inside():
     cache.k_pages.zero_()
     cache.v_pages.zero_()
     big = 2 ** 31 - 1
-    for rows in (5, 400):
+    for rows in (5, 50, 400):
         raw = torch.full((rows + 64, 8, 32), 3.0, dtype=BF, device="cuda")
         q, o = rand((rows, 8, 32), BF, g), raw[32:32 + rows]
         for off, seq, kb, ke in (([5, 0, 9], [0, 1], [0, 0], [200, 200]), ([-4, 2, big], [0, 1], [-5, 3], [big, 60]),
@@ -311,7 +311,7 @@ def test_attend_same_bits_again_and_on_another_stream():
     kp, vp = ref.pools(60, 2, 48, BF, g)
     table = ref.table_of([50, 9], 60, g)
     cache = PagedCache(16, 2, 48, 60, k_pages=kp, v_pages=vp)
-    for n in (1, 3, 300):
+    for n in (1, 3, 20, 300):
         q = rand((2 * n, 16, 48), BF, g)
         args = (q, table if n != 3 else widened(table), ref.i32([0, n, 2 * n]), ref.i32([0, 5]), ref.i32([6001, 1100]))
         first = cache.attend(*args, causal=True)
@@ -326,7 +326,7 @@ def test_attend_same_bits_again_and_on_another_stream():
             assert torch.equal(o, first)
 
 
-@pytest.mark.parametrize("most", [1, 4, 200])
+@pytest.mark.parametrize("most", [1, 4, 40, 200])
 def test_captured_step_replays_for_other_lengths(most):
     """Write and attend in one graph; lengths, tables and positions change between replays."""
     g = gen(13)
@@ -364,7 +364,7 @@ def test_captured_step_replays_for_other_lengths(most):
 
 def test_workspace_and_outputs_are_not_overrun():
     g = gen(14)
-    for n, hq, hkv, d in ((1, 16, 1, 24), (2, 12, 1, 48), (3, 16, 1, 32), (100, 8, 2, 48)):
+    for n, hq, hkv, d in ((1, 16, 1, 24), (2, 12, 1, 48), (3, 16, 1, 32), (10, 16, 1, 24), (100, 8, 2, 48)):
         kp, vp = ref.pools(30, hkv, d, BF, g)
         cache = PagedCache(hq, hkv, d, 30, k_pages=kp, v_pages=vp)
         table = widened(ref.table_of([30], 30, g))
@@ -384,7 +384,7 @@ def test_workspace_and_outputs_are_not_overrun():
             assert (r[:4096] == 0xA5).all() and (r[4096 + b:] == 0xA5).all()
 
 
-@pytest.mark.parametrize("rows,wide", [(1, False), (1, True), (200, False)])
+@pytest.mark.parametrize("rows,wide", [(1, False), (1, True), (12, False), (200, False)])
 def test_forced_timeout_is_reported_and_the_context_stays_usable(rows, wide):
     g = gen(15)
     kp, vp = ref.pools(4, 2, 48, BF, g)
@@ -516,7 +516,7 @@ def test_large_values_survive_a_moving_reference():
     for i, p in enumerate(table[0].tolist()):
         kp[0, p] *= 0.5 + 2 * i
     cache = PagedCache(8, 1, d, 12, k_pages=kp, v_pages=vp)
-    for n in (1, 5, 60):
+    for n in (1, 5, 20, 60):
         q = rand((n, 8, d), BF, g)
         o = cache.attend(q, table, ref.i32([0, n]), ref.i32([0]), ref.i32([1500]), causal=True)
         assert cache.status() == _abi.BCA_OK
@@ -586,7 +586,7 @@ def test_calls_on_two_streams_at_once():
     cache = PagedCache(16, 2, 48, 80, k_pages=kp, v_pages=vp)
     table = widened(ref.table_of([40, 40], 80, g))
     calls = []
-    for n in (1, 4, 500):
+    for n in (1, 4, 20, 500):
         q = rand((2 * n, 16, 48), BF, g)
         calls.append((q, table, ref.i32([0, n, 2 * n]), ref.i32([3, 0]), ref.i32([5001, 4700])))
     want = [cache.attend(*c, causal=True) for c in calls]
