@@ -189,9 +189,11 @@ template <int R>
 __device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, uint32_t &lo, uint32_t &hi, uint32_t &total,
                                              PagedCursor<R> &cur) {
     const int lane = threadIdx.x & 31;
-    PagedSlice s;
+    // Up to 32 slices stay in the lanes' registers; of more, four loads are on the way at a time
+    // here, and the next 32 while 32 are looked through below.
+    PagedSlice s, ahead;
     uint32_t mine = 0, sum = 0;
-#pragma unroll 1
+#pragma unroll 4
     for (int i = lane; i < a.slices; i += 32) {
         s = paged_slice<R>(a, i);
         mine = (uint32_t)a.hkv * s.upto(s.tiles);
@@ -205,14 +207,13 @@ __device__ __forceinline__ bool paged_locate(const PagedArgs &a, int c, uint32_t
     // (offsets that do not rise may make the whole longer than 2^32, and then nothing be found)
     uint32_t carry = 0, pre = 0;
     int src = -1;
+    if (a.slices > 32) ahead = paged_slice<R>(a, lane);
 #pragma unroll 1
     for (int base = 0; base < a.slices && src < 0; base += 32) {
         if (a.slices > 32) {
-            mine = 0;
-            if (base + lane < a.slices) {
-                s = paged_slice<R>(a, base + lane);
-                mine = (uint32_t)a.hkv * s.upto(s.tiles);
-            }
+            s = ahead;
+            mine = base + lane < a.slices ? (uint32_t)a.hkv * s.upto(s.tiles) : 0u;
+            if (base + 32 + lane < a.slices) ahead = paged_slice<R>(a, base + 32 + lane);
         }
         uint32_t inc = mine;
 #pragma unroll
