@@ -120,17 +120,31 @@ int bca_paged_copy(bca_paged_t cache, const int32_t *pairs, int64_t n, void *k_p
     const PagedCache &c = cache->cache;
     if (n > 0 && !pairs) return BCA_ERR_INVALID_ARGUMENT;
     if (n > c.pages) return BCA_ERR_BAD_PAGE;  // some page would be written twice
+    for (int64_t i = 0; i < 2 * n; ++i)
+        if (pairs[i] < 0 || pairs[i] >= c.pages) return BCA_ERR_BAD_PAGE;
     try {
-        std::vector<int32_t> to((size_t)n);
-        for (int64_t i = 0; i < n; ++i) {
-            for (int e = 0; e < 2; ++e)
-                if (pairs[2 * i + e] < 0 || pairs[2 * i + e] >= c.pages) return BCA_ERR_BAD_PAGE;
-            to[(size_t)i] = pairs[2 * i + 1];
+        // Which pages are written: a bit each (1,000 moves in a pool of 2,000 pages: 2 us), or, where
+        // the pool is far larger than the call, a sorted list (the same moves: 40 us).
+        if (c.pages / 64 <= 4096 + 64 * n) {
+            std::vector<uint64_t> written((size_t)(c.pages / 64 + 1), 0);
+            for (int64_t i = 0; i < n; ++i) {
+                const uint32_t to = (uint32_t)pairs[2 * i + 1];
+                const uint64_t bit = 1ull << (to % 64);
+                if (written[to / 64] & bit) return BCA_ERR_BAD_PAGE;
+                written[to / 64] |= bit;
+            }
+            for (int64_t i = 0; i < n; ++i) {
+                const uint32_t from = (uint32_t)pairs[2 * i];
+                if (written[from / 64] >> (from % 64) & 1) return BCA_ERR_BAD_PAGE;
+            }
+        } else {
+            std::vector<int32_t> to((size_t)n);
+            for (int64_t i = 0; i < n; ++i) to[(size_t)i] = pairs[2 * i + 1];
+            std::sort(to.begin(), to.end());
+            if (std::adjacent_find(to.begin(), to.end()) != to.end()) return BCA_ERR_BAD_PAGE;
+            for (int64_t i = 0; i < n; ++i)
+                if (std::binary_search(to.begin(), to.end(), pairs[2 * i])) return BCA_ERR_BAD_PAGE;
         }
-        std::sort(to.begin(), to.end());
-        if (std::adjacent_find(to.begin(), to.end()) != to.end()) return BCA_ERR_BAD_PAGE;
-        for (int64_t i = 0; i < n; ++i)
-            if (std::binary_search(to.begin(), to.end(), pairs[2 * i])) return BCA_ERR_BAD_PAGE;
     } catch (const std::bad_alloc &) {
         return BCA_ERR_NO_MEMORY;
     }

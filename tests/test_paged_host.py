@@ -87,9 +87,11 @@ def test_null_arguments_and_a_host_only_cache():
     ([(0, 1), (1, 2)], _abi.BCA_ERR_BAD_PAGE), ([(3, 3)], _abi.BCA_ERR_BAD_PAGE),
     ([(0, 1)] * 11, _abi.BCA_ERR_BAD_PAGE), ([(1, 2), (2, 1)], _abi.BCA_ERR_BAD_PAGE)])
 def test_page_moves_are_checked_before_anything_else(pairs, code):
-    c = PagedCache(16, 2, 48, 10, host_only=True)
     a = np.asarray(pairs, np.int32).reshape(-1, 2)
-    assert _abi.lib().bca_paged_copy(c._h, a.ctypes.data, len(a), None, None, None) == code
+    for pages in (10, 10_000_000):               # a bit a page, and a sorted list
+        c = PagedCache(16, 2, 48, pages, host_only=True)
+        b = np.where(a == 10, pages, a).astype(np.int32)
+        assert _abi.lib().bca_paged_copy(c._h, b.ctypes.data, len(b), None, None, None) == code
     assert "page" in _abi.error_string(_abi.BCA_ERR_BAD_PAGE)
 
 
