@@ -33,7 +33,10 @@ constexpr int kWarps = 8;                     // consumers; one more fills the r
 constexpr int kThreads = (kWarps + 1) * 32;
 constexpr int kWarpTokens = kPage / kWarps;   // 16
 
-template <int D, int MT, int CL>
+// LO: fp16 values; the rounding of queries made here is kept as a second fp16 tile (paged_tiles.cu has
+// the reason).  Given post-prologue they take no time for it (24.7 us both ways, 64 rows); made here
+// they take 26.8 us against 24.8.
+template <int D, int MT, int CL, bool LO>
 struct RowsSmem {
     static constexpr int TILE = D * kPage * 2;
     // one block a multiprocessor with all of its shared memory; of a cluster's blocks two (D < 48)
@@ -41,7 +44,8 @@ struct RowsSmem {
     static constexpr int QSTRIDE = D == 24 ? 40 : D + 8;  // elements; an odd number of 16-byte units
     static constexpr int OFF_RING = 0;
     static constexpr int OFF_Q = STAGES * 2 * TILE;
-    static constexpr int OFF_MERGE = OFF_Q + 16 * MT * QSTRIDE * 2;
+    static constexpr int Q_BYTES = 16 * MT * QSTRIDE * 2;
+    static constexpr int OFF_MERGE = OFF_Q + (LO ? 2 : 1) * Q_BYTES;
     static constexpr int OFF_PART = OFF_MERGE + kWarps * 16 * (D + 2) * 4;  // the block's, for its cluster
     static constexpr int OFF_BAR = OFF_PART + (CL == 1 ? 0 : 16 * MT * (D + 2) * 4);
     static constexpr int OFF_HERE = OFF_BAR + 2 * (STAGES + kItemRing) * 8;
@@ -81,7 +85,7 @@ __device__ __forceinline__ float cluster_load(uint32_t addr, int rank) {
 // cluster; 1: the blocks take equal shares of all items.
 template <int D, typename T, int MT, int CL>
 __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_constant__ PagedArgs a) {
-    using L = RowsSmem<D, MT, CL>;
+    using L = RowsSmem<D, MT, CL, Io<T>::kF16>;
     constexpr int S = L::STAGES;
     constexpr int R = 16 * MT;
     constexpr int KS = D / 16;            // 16-channel steps; D = 24 has an 8-channel one behind
@@ -163,8 +167,9 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         if (p0 < 0) break;
 
         // queries: QK-Norm and RoPE, fp16 (|q_hat| <= sqrt(D) max|gain|; 11 bits of significand
-        // against bf16's 8).  The softmax scale is applied to the scores in fp32 instead, so that
-        // bf16 queries given post-prologue stay exact.
+        // against bf16's 8), with what the rounding left where values are fp16.  The
+        // softmax scale is applied to the scores in fp32 instead, so that bf16 queries given
+        // post-prologue stay exact.
         for (int r = threadIdx.x >> 3; r < R; r += kWarps * 4) {
             const int e = lane & 7;
             const bool live = r < x.left;  // the same for the eight lanes of a row
@@ -176,9 +181,16 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
             if (a.pos) q.prologue(gain, a.turns, a.eps, e);
 #pragma unroll
             for (int i = 0; i < Row8<D>::N; ++i)
-                if (e + 8 * i < D / 2)
-                    *reinterpret_cast<uint32_t *>(qs + r * L::QSTRIDE + 2 * (e + 8 * i)) =
-                        live ? pack_f16x2(q.x[i].x, q.x[i].y) : 0u;
+                if (e + 8 * i < D / 2) {
+                    __half *at = qs + r * L::QSTRIDE + 2 * (e + 8 * i);
+                    const float2 y = live ? q.x[i] : float2{0.f, 0.f};
+                    const uint32_t hi = pack_f16x2(y.x, y.y);
+                    *reinterpret_cast<uint32_t *>(at) = hi;
+                    if (Io<T>::kF16 && a.pos) {
+                        const float2 back = Io<__half>::unpack(hi);
+                        *reinterpret_cast<uint32_t *>(at + L::Q_BYTES / 2) = pack_f16x2(y.x - back.x, y.y - back.y);
+                    }
+                }
         }
         consumers_sync();
         uint32_t qa[MT][KS][4], qt[MT][2];
@@ -243,6 +255,24 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
                     for (int m = 0; m < MT; ++m) {
                         mma8_f16(s[m][0], qt[m][0], qt[m][1], kt[0]);
                         mma8_f16(s[m][1], qt[m][0], qt[m][1], kt[1]);
+                    }
+                }
+                if (Io<T>::kF16 && a.pos) {
+#pragma unroll
+                    for (int m = 0; m < MT; ++m) {
+                        const __half *q0 = qs + L::Q_BYTES / 2 + (16 * m + g) * L::QSTRIDE + 2 * t;
+                        auto word = [&](int at) { return *reinterpret_cast<const uint32_t *>(q0 + at); };
+#pragma unroll
+                        for (int k = 0; k < KS; ++k) {
+                            const uint32_t lo[4] = {word(16 * k), word(8 * L::QSTRIDE + 16 * k), word(16 * k + 8),
+                                                    word(8 * L::QSTRIDE + 16 * k + 8)};
+                            mma16<true>(s[m][0], lo, kf[k][0], kf[k][1]);
+                            mma16<true>(s[m][1], lo, kf[k][2], kf[k][3]);
+                        }
+                        if constexpr (TAIL) {
+                            mma8_f16(s[m][0], word(16 * KS), word(8 * L::QSTRIDE + 16 * KS), kt[0]);
+                            mma8_f16(s[m][1], word(16 * KS), word(8 * L::QSTRIDE + 16 * KS), kt[1]);
+                        }
                     }
                 }
                 if (!inside) {
@@ -423,11 +453,17 @@ const void *rows_kernel(int rows, bool cluster) {
     return rows == 16 ? (const void *)paged_rows_kernel<D, T, 1, 1> : (const void *)paged_rows_kernel<D, T, 2, 1>;
 }
 
+template <int D, typename T>
+int rows_bytes(int rows, bool cluster) {
+    constexpr bool LO = Io<T>::kF16;
+    return cluster      ? RowsSmem<D, 1, kCluster, LO>::BYTES
+           : rows == 16 ? RowsSmem<D, 1, 1, LO>::BYTES
+                        : RowsSmem<D, 2, 1, LO>::BYTES;
+}
+
 template <int D>
 const void *rows_kernel(bool f16, int rows, bool cluster, int &bytes) {
-    bytes = cluster      ? RowsSmem<D, 1, kCluster>::BYTES
-            : rows == 16 ? RowsSmem<D, 1, 1>::BYTES
-                         : RowsSmem<D, 2, 1>::BYTES;
+    bytes = f16 ? rows_bytes<D, __half>(rows, cluster) : rows_bytes<D, __nv_bfloat16>(rows, cluster);
     return f16 ? rows_kernel<D, __half>(rows, cluster) : rows_kernel<D, __nv_bfloat16>(rows, cluster);
 }
 

@@ -35,7 +35,15 @@ namespace {
 // SL: 128-row tiles that share a page.  Three make a block that fills a multiprocessor; with one,
 // for slices of 65 to 256 rows, two blocks share it (a block of three with one tile at work had a
 // softmax warp a scheduler: 114 against 83 us for 16 sequences of 8,000 tokens, 128 rows each).
-template <int D, int SL>
+//
+// LO: fp16 values and a prologue.  There a query rounded to fp16 after QK-Norm and RoPE would cost
+// as much again as the roundings of P and of O (0.00036 against 0.00021 of plain fp32 relative to
+// |O|), so what the rounding leaves is kept too, as a second fp16 tile, and S gets both products:
+// 0.00029, for 400 us as before (24 heads over 6 ragged sequences, D = 32), 945 against 882 (6,144 new
+// tokens over 18,432, D = 24) and 2,455 against 2,199 (10,800 over 32,400, D = 48).  Beside bf16's
+// roundings it would not show, and queries given post-prologue are exact; those keep the single tile
+// by a template argument, since a branch in the kernel cost them 12 %.
+template <int D, int SL, bool LO>
 struct TilesSmem {
     static constexpr int ROWS = 128 * SL;
     static constexpr int BUFFERS = SL == 1 ? 2 : 4;  // S tiles of 128 x 128 in tensor memory, used in turn
@@ -44,10 +52,12 @@ struct TilesSmem {
     static constexpr int TILE = D * kPage * 2;       // bytes of a page's K or V of one head
     static constexpr int KSTAGE = DPAD * kPage * 2;  // K is padded to whole 16-channel steps
     static constexpr int STAGE = KSTAGE + TILE;
-    static constexpr int STAGES = SL == 1 ? (D == 48 ? 3 : 5) : (D == 48 ? 6 : 8);
+    static constexpr int STAGES = SL == 1 ? (D == 48 ? 3 : 5) - (LO && D >= 32 ? 1 : 0)
+                                          : D == 48 ? (LO ? 3 : 6) : D == 32 && LO ? 7 : 8;
     static constexpr int Q_BYTES = 128 * DPAD * 2;
     static constexpr int OFF_Q = 0;
-    static constexpr int Q_ITEM = SL * Q_BYTES;
+    static constexpr int Q_TILE = (LO ? 2 : 1) * Q_BYTES;  // of 128 rows
+    static constexpr int Q_ITEM = SL * Q_TILE;
     static constexpr int OFF_RING = 2 * Q_ITEM;      // queries of this item and of the next
     static constexpr int OFF_BAR = OFF_RING + STAGES * STAGE;
     static constexpr int B_FULL = 0;
@@ -87,10 +97,10 @@ __device__ __forceinline__ void tmem_ld_frag(uint32_t taddr, float (&f)[4][4]) {
 
 // QK-Norm and RoPE of 16 packed rows of an item, from row `first` on, into the A operand of
 // S = Q K^T (fp16, K-major core matrices, tiles of 128 rows); a warp, eight lanes a row.
-template <int D, typename T>
+template <int D, typename T, bool LO>
 __device__ __forceinline__ void query_rows(const PagedArgs &a, const PagedItem &x, const float2 (&gain)[Row8<D>::N],
                                            uint8_t *to, int first) {
-    constexpr int kTile = TilesSmem<D, 1>::Q_BYTES;
+    using L = TilesSmem<D, 1, LO>;
     const int e = threadIdx.x & 7, r0 = first + (threadIdx.x >> 3 & 3);
     Row8<D> q[4];
 #pragma unroll
@@ -98,26 +108,33 @@ __device__ __forceinline__ void query_rows(const PagedArgs &a, const PagedItem &
         const uint32_t packed = x.head + min(r0 + 4 * i, x.left - 1);
         const int64_t row = x.row + x.token + (int32_t)(packed / a.group);
         q[i].load(static_cast<const T *>(a.q) + (row * a.hq + x.g * a.group + packed % a.group) * D,
-                  a.pos ? a.pos + row * 3 : static_cast<const int32_t *>(a.q), e);
+                  LO || a.pos ? a.pos + row * 3 : static_cast<const int32_t *>(a.q), e);
     }
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int r = r0 + 4 * i;
-        if (a.pos) q[i].prologue(gain, a.turns, a.eps, e);
+        if (LO || a.pos) q[i].prologue(gain, a.turns, a.eps, e);
 #pragma unroll
         for (int k = 0; k < Row8<D>::N; ++k) {
             const int pr = e + 8 * k;
-            if (pr < D / 2)
-                *reinterpret_cast<uint32_t *>(to + r / 128 * kTile + (pr >> 2) * 2048 + r % 128 * 16 +
-                                              (pr & 3) * 4) = r < x.left ? pack_f16x2(q[i].x[k].x, q[i].x[k].y) : 0u;
+            if (pr < D / 2) {
+                uint8_t *at = to + r / 128 * L::Q_TILE + (pr >> 2) * 2048 + r % 128 * 16 + (pr & 3) * 4;
+                const float2 y = r < x.left ? q[i].x[k] : float2{0.f, 0.f};
+                const uint32_t hi = pack_f16x2(y.x, y.y);
+                *reinterpret_cast<uint32_t *>(at) = hi;
+                if constexpr (LO) {
+                    const float2 back = Io<__half>::unpack(hi);
+                    *reinterpret_cast<uint32_t *>(at + L::Q_BYTES) = pack_f16x2(y.x - back.x, y.y - back.y);
+                }
+            }
         }
     }
 }
 
-template <int D, typename T, int SL>
-__global__ void __launch_bounds__(TilesSmem<D, SL>::THREADS, SL == 1 ? 2 : 1)
+template <int D, typename T, int SL, bool LO>
+__global__ void __launch_bounds__(128 + 128 * SL, SL == 1 ? 2 : 1)
     paged_tiles_kernel(const __grid_constant__ PagedArgs a) {
-    using L = TilesSmem<D, SL>;
+    using L = TilesSmem<D, SL, LO>;
     constexpr int kSlots = SL, kBuffers = L::BUFFERS, kRows = L::ROWS, kThreads = L::THREADS;
     constexpr int S = L::STAGES;
     constexpr int NV = D / 8;
@@ -159,7 +176,7 @@ __global__ void __launch_bounds__(TilesSmem<D, SL>::THREADS, SL == 1 ? 2 : 1)
     if constexpr (L::DPAD > D) {
         // channels that do not exist: zero in Q and, so that 0 times them is 0, in every K stage
         constexpr int N = (L::KSTAGE - L::TILE) / 16;
-        for (int i = threadIdx.x; i < (S + 2 * kSlots) * N; i += kThreads) {
+        for (int i = threadIdx.x; i < (S + 2 * L::Q_ITEM / L::Q_BYTES) * N; i += kThreads) {
             uint8_t *to = i / N < S ? smem + L::OFF_RING + i / N * L::STAGE + L::TILE
                                     : smem + L::OFF_Q + (i / N - S) * L::Q_BYTES + 128 * D * 2;
             reinterpret_cast<uint4 *>(to)[i % N] = make_uint4(0, 0, 0, 0);
@@ -213,12 +230,17 @@ __global__ void __launch_bounds__(TilesSmem<D, SL>::THREADS, SL == 1 ? 2 : 1)
                         if (!ok) continue;
                         ++made;
                         tc_fence_after();
-                        const uint32_t qa = sbase + L::OFF_Q + qb * L::Q_ITEM + s * L::Q_BYTES;
+                        const uint32_t qa = sbase + L::OFF_Q + qb * L::Q_ITEM + s * L::Q_TILE;
                         const uint32_t kb = sbase + L::OFF_RING + st * L::STAGE;
 #pragma unroll
                         for (int k = 0; k < L::DPAD / 16; ++k)
                             mma_f16(tbase + 128 * buf, smem_desc(qa + k * 4096, 2048, 128),
                                     smem_desc(kb + k * 4096, 2048, 128), IDESC, k > 0);
+                        if constexpr (LO)
+#pragma unroll
+                            for (int k = 0; k < L::DPAD / 16; ++k)
+                                mma_f16(tbase + 128 * buf, smem_desc(qa + L::Q_BYTES + k * 4096, 2048, 128),
+                                        smem_desc(kb + k * 4096, 2048, 128), IDESC, 1);
                         mma_commit(bar(L::B_S_FULL + s * kBuffers + buf));
                     }
                 }
@@ -265,7 +287,7 @@ __global__ void __launch_bounds__(TilesSmem<D, SL>::THREADS, SL == 1 ? 2 : 1)
                     const int rows = min((x.left + 127) / 128 * 128, kRows);
 #pragma unroll 1
                     for (int r = (warp - 2) * 16; r < rows; r += 32)
-                        query_rows<D, T>(a, x, gain, smem + L::OFF_Q + qb * L::Q_ITEM, r);
+                        query_rows<D, T, LO>(a, x, gain, smem + L::OFF_Q + qb * L::Q_ITEM, r);
                     fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(bar(L::B_Q_FULL + qb));
@@ -306,7 +328,7 @@ __global__ void __launch_bounds__(TilesSmem<D, SL>::THREADS, SL == 1 ? 2 : 1)
                 float2 gain[Row8<D>::N];
                 Row8<D>::load_gain(a.q_gain, lane & 7, gain);
 #pragma unroll 1
-                for (int r = wr; r < wr + 32; r += 16) query_rows<D, T>(a, x, gain, smem + L::OFF_Q, r);
+                for (int r = wr; r < wr + 32; r += 16) query_rows<D, T, LO>(a, x, gain, smem + L::OFF_Q, r);
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(bar(L::B_Q_FIRST));
@@ -641,38 +663,43 @@ __global__ void __launch_bounds__(TilesSmem<D, SL>::THREADS, SL == 1 ? 2 : 1)
     }
 }
 
-template <int D>
-const void *tiles_kernel(bool f16, bool narrow, int &bytes) {
-    bytes = narrow ? TilesSmem<D, 1>::BYTES : TilesSmem<D, 3>::BYTES;
-    if (narrow)
-        return f16 ? (const void *)paged_tiles_kernel<D, __half, 1> : (const void *)paged_tiles_kernel<D, __nv_bfloat16, 1>;
-    return f16 ? (const void *)paged_tiles_kernel<D, __half, 3> : (const void *)paged_tiles_kernel<D, __nv_bfloat16, 3>;
+template <int D, typename T, int SL, bool LO>
+const void *tiles_kernel(int &bytes) {
+    bytes = TilesSmem<D, SL, LO>::BYTES;
+    return (const void *)paged_tiles_kernel<D, T, SL, LO>;
 }
 
-const void *tiles_kernel(const PagedCache &c, int rows, int &bytes) {
+template <int D, int SL>
+const void *tiles_kernel(bool f16, bool prologue, int &bytes) {
+    if (!f16) return tiles_kernel<D, __nv_bfloat16, SL, false>(bytes);
+    return prologue ? tiles_kernel<D, __half, SL, true>(bytes) : tiles_kernel<D, __half, SL, false>(bytes);
+}
+
+const void *tiles_kernel(const PagedCache &c, int rows, bool prologue, int &bytes) {
     const bool f16 = (c.flags & BCA_PAGED_FP16) != 0, narrow = rows == kPagedNarrowRows;
     switch (c.d) {
-        case 24: return tiles_kernel<24>(f16, narrow, bytes);
-        case 32: return tiles_kernel<32>(f16, narrow, bytes);
-        default: return tiles_kernel<48>(f16, narrow, bytes);
+        case 24: return narrow ? tiles_kernel<24, 1>(f16, prologue, bytes) : tiles_kernel<24, 3>(f16, prologue, bytes);
+        case 32: return narrow ? tiles_kernel<32, 1>(f16, prologue, bytes) : tiles_kernel<32, 3>(f16, prologue, bytes);
+        default: return narrow ? tiles_kernel<48, 1>(f16, prologue, bytes) : tiles_kernel<48, 3>(f16, prologue, bytes);
     }
 }
 
 }  // namespace
 
 int prepare_paged_tiles(const PagedCache &c) {
-    for (int rows : {kPagedNarrowRows, kPagedTileRows}) {
-        int bytes = 0;
-        const void *f = tiles_kernel(c, rows, bytes);
-        if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
-            return BCA_ERR_CUDA;
-    }
+    for (int rows : {kPagedNarrowRows, kPagedTileRows})
+        for (bool prologue : {false, true}) {
+            int bytes = 0;
+            const void *f = tiles_kernel(c, rows, prologue, bytes);
+            if (cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes) != cudaSuccess)
+                return BCA_ERR_CUDA;
+        }
     return BCA_OK;
 }
 
 int launch_paged_tiles(const PagedCache &c, const PagedArgs &a, cudaStream_t stream) {
     int bytes = 0;
-    const void *f = tiles_kernel(c, a.rows, bytes);
+    const void *f = tiles_kernel(c, a.rows, a.pos != nullptr, bytes);
     PagedArgs args = a;
     void *params[] = {&args};
     return cudaLaunchKernel(f, dim3((unsigned)paged_shares(a.rows)), dim3((unsigned)(128 + a.rows)), params,
