@@ -211,6 +211,31 @@ def test_attend_scores_that_grow_and_shrink():
         no_worse(lse, wl, bl, "lse")
 
 
+@pytest.mark.parametrize("d", [24, 32, 48])
+@pytest.mark.parametrize("rows", [1, 20, 100, 400])
+def test_attend_fp16_queries_keep_their_rounding(d, rows):
+    """Over a single key the LSE is the score, so it shows the queries' precision alone.  Per element,
+    relative to its RoPE pair's length: sine and cosine 2^-21.2 and 2^-21.4 (CUDA's bounds for the fast
+    ones) with 2^-22 each for the angle in fp32, together below 2^-19.6; RMS norm, gain and RoPE's
+    products and sum, six roundings, 2^-21.4; the second fp16 tile 2^-22; the sum of d <= 48 products in
+    fp32, 2^-18.4; scale and LSE 2^-22.  Below 2^-17 in all; an fp16 rounding alone is 2^-11."""
+    g = gen(d + rows)
+    hq, hkv, key = 4, 2, 5
+    kp, vp = ref.pools(2, hkv, d, HF, g)
+    table = ref.table_of([1], 2, g)
+    cache = PagedCache(hq, hkv, d, 2, dtype=HF, k_pages=kp, v_pages=vp)
+    q, pos = rand((rows, hq, d), HF, g), positions(rows, g)
+    gain = 1 + 0.1 * torch.randn(d, generator=g, device="cuda")
+    lse = torch.full((hq, rows), math.nan, device="cuda")
+    cache.attend(q, table, ref.i32([0, rows]), ref.i32([key]), ref.i32([key + 1]), pos=pos, q_gain=gain, lse=lse)
+    assert cache.status() == _abi.BCA_OK
+    keys, _ = ref.unpage(kp[0], vp[0], table[0].tolist(), PAGE)
+    k = keys[key].double().repeat_interleave(hq // hkv, 0)
+    qh = ref.prologue(q, pos, gain)
+    pair = qh.unflatten(-1, (d // 2, 2)).norm(dim=-1, keepdim=True).expand(-1, -1, -1, 2).flatten(-2)
+    no_worse(lse, (qh * k).sum(-1).T / math.sqrt(d), 2.0 ** -17 * (pair * k.abs()).sum(-1).T / math.sqrt(d), "lse")
+
+
 @pytest.mark.parametrize("rows", [1, 5, 40, 150])
 @pytest.mark.parametrize("dtype", [BF, HF])
 def test_attend_empty_slices_and_rows_left_alone(rows, dtype):
