@@ -283,6 +283,11 @@ int launch_copy(const CopyArgs &a, const PagedCache &c, const int32_t *pairs, in
 // and sums, a lane each, then O, eight lanes a piece, with the loads of 32 pieces on the way
 // at a time: three trips to memory whatever their number up to 32, and two, four rows a warp,
 // for up to four.
+//
+// "No keys" is a sum of exactly 0: a key with a finite score adds at least its own weight, and one
+// whose score is NaN leaves NaN in the sum and in O, while the reference, a running maximum, stays
+// where it was, at -inf if nothing else was seen.  A piece whose sum is NaN takes part: its weight,
+// 2^(-inf - r) = 0 or, beside nothing finite, NaN, times NaN is NaN in the sum and in O.
 
 // Calls that go by clusters: 16-row tiles, few items, tables up to this wide.  Measured with one
 // query token, us by clusters / by shares, D = 24 and D = 48:
@@ -317,7 +322,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) paged_join_kernel(const __gri
     const int rows = a.rows / gridDim.y, row_end = min((int)(blockIdx.y + 1) * rows, j.left);
     // O / l and the LSE of a row, eight lanes
     auto write = [&](int row, float ref, float sum, const float (&o)[D / 8]) {
-        const bool none = ref == -INFINITY;
+        const bool none = ref == -INFINITY && sum == 0.f;
         const float inv = none ? 0.f : 1.f / sum;
         const uint32_t packed = j.head + row;
         const int64_t token = (int64_t)j.row + j.token + (int32_t)(packed / a.group);
@@ -355,7 +360,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) paged_join_kernel(const __gri
             for (int x = 1; x < kJoinFew; ++x) top = fmaxf(top, r[x]);
 #pragma unroll
             for (int x = 0; x < kJoinFew; ++x) {
-                if (r[x] == -INFINITY) continue;  // a piece without keys: it has no O, and may have no sum
+                if (l[x] == 0.f) continue;  // a piece without keys: it may have no O
                 const float w = sm100::ex2(r[x] - top);
                 sum = fmaf(l[x], w, sum);
 #pragma unroll
@@ -380,10 +385,11 @@ __global__ void __launch_bounds__(kJoinThreads, 3) paged_join_kernel(const __gri
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, s));
             top = fmaxf(top, ref);
-            if (top == -INFINITY) continue;
+            const bool some = l != 0.f;  // else a piece without keys: it may have no O
+            if (!__any_sync(0xffffffffu, some)) continue;
             const float keep = ref == -INFINITY ? 0.f : sm100::ex2(ref - top);
-            const float w = r == -INFINITY ? 0.f : sm100::ex2(r - top);
-            l = r == -INFINITY ? 0.f : l * w;  // (a piece without keys may have no sum)
+            const float w = some ? sm100::ex2(r - top) : 0.f;
+            if (some) l *= w;
 #pragma unroll
             for (int s = 16; s > 0; s >>= 1) l += __shfl_xor_sync(0xffffffffu, l, s);
             sum = sum * keep + l;
@@ -393,7 +399,7 @@ __global__ void __launch_bounds__(kJoinThreads, 3) paged_join_kernel(const __gri
 #pragma unroll
             for (int i = 0; i < 8; ++i) {
                 const int z = base + 4 * i + sub;
-                const bool on = __shfl_sync(0xffffffffu, r, 4 * i + sub) != -INFINITY && z < pieces;
+                const bool on = __shfl_sync(0xffffffffu, some, 4 * i + sub);
                 const float *from = first + (2 * (size_t)(c + z) + (z == 0 ? 1 : 0)) * slot;
 #pragma unroll
                 for (int k = 0; k < D / 8; ++k) y[i][k] = on ? from[8 * k] : 0.f;

@@ -528,7 +528,10 @@ __device__ __forceinline__ void paged_fill(const PagedArgs &a, int c, uint32_t r
     if (CL == 1 && !more) {
         // an empty stretch inside an item that others share: a piece without keys
         if (lane == 0) a.joins[c].last = -1;
-        for (int r = lane; r < R; r += 32) paged_part(a, D, 2 * c)[R * D + r] = -INFINITY;
+        for (int r = lane; r < R; r += 32) {
+            paged_part(a, D, 2 * c)[R * D + r] = -INFINITY;
+            paged_part(a, D, 2 * c)[R * (D + 1) + r] = 0.f;
+        }
     }
     // An item is published when the ring's worth of pages of the one before it is on the way, so
     // that no page waits for it; for the 384-row tiles before those pages, since two warps need the

@@ -138,7 +138,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
     Row8<D>::load_gain(a.q_gain, lane & 7, gain);
     // O / l and the LSE of row r of an item: channels e, e + 16, .. of 16 lanes
     auto write = [&](const PagedItem &x, int r, int e, float top, float l, const float (&y)[(D + 15) / 16]) {
-        const bool none = top == -INFINITY;
+        const bool none = top == -INFINITY && l == 0.f;  // a row whose scores are all NaN has a sum that is NaN
         const float inv = none ? 0.f : 1.f / l;
         const uint32_t packed = x.head + r;
         const int64_t token = x.row + x.token + (int32_t)(packed / a.group);
@@ -392,7 +392,7 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
             } else if (16 * m + r < x.left) {
                 if (x.whole) {
                     write(x, 16 * m + r, e, top, l, y);
-                } else {  // without pages too: the reference, -inf, tells
+                } else {  // without pages too: the sum, 0, tells
                     float *part = paged_part(a, D, x.part);
 #pragma unroll
                     for (int i = 0; i < (D + 15) / 16; ++i)

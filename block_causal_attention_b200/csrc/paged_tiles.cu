@@ -622,7 +622,7 @@ __global__ void __launch_bounds__(128 + 128 * SL, SL == 1 ? 2 : 1)
                     const int r = wr + 16 * m + 8 * h + g;
                     if (r >= x.left) continue;
                     if (x.whole) {
-                        const bool none = ref[m][h] == -INFINITY;
+                        const bool none = ref[m][h] == -INFINITY && l == 0.f;  // (NaN scores leave a NaN in l)
                         const float inv = none ? 0.f : 1.f / l;
                         const uint32_t packed = x.head + r;
                         const int64_t token = x.row + x.token + (int32_t)(packed / a.group);
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(128 + 128 * SL, SL == 1 ? 2 : 1)
                         }
                         if (a.lse && t == 0)
                             a.lse[head * a.nq + token] = none ? -INFINITY : (ref[m][h] + log2f(l)) * 0.69314718055994531f;
-                    } else {  // without pages too: the reference, -inf, tells
+                    } else {  // without pages too: the sum, 0, tells
 #pragma unroll
                         for (int n = 0; n < NV; ++n)
                             *reinterpret_cast<float2 *>(part + (size_t)r * D + 8 * n + 2 * t) =

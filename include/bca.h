@@ -417,7 +417,8 @@ int bca_paged_copy(bca_paged_t cache, const int32_t *pairs, int64_t n, void *k_p
  *            outside [0, seqs) is a slice that sees no key, or NULL: slice i reads row i;
  *   k_begin, k_end: device int32 [slices]
  *   lse    : fp32 [Hq][nq] natural log, or NULL (not wanted)
- * Rows that see no key get O = 0 and LSE = -inf; rows of q outside every slice are neither
+ * Rows that see no key get O = 0 and LSE = -inf (so does a row whose every score is -inf), rows
+ * with a score that is NaN get NaN in O and LSE; rows of q outside every slice are neither
  * read nor written.  What pages hold outside a row's own keys never reaches the row, NaN and
  * infinities included.  workspace: bca_paged_workspace_bytes bytes (which may be 0: NULL then),
  * 16-byte aligned; calls that may overlap on the GPU need one each.  Results do not depend on timing: the same call
