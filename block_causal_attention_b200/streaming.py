@@ -128,6 +128,7 @@ class PagedStep:
     k_begin: Any
     k_end: Any
     pos: Any                 # [rows, 3]
+    made: Tuple[int, ...]    # when the videos' pages last changed hands, as ``begin`` found it
 
 
 class PagedWindow:
@@ -138,7 +139,11 @@ class PagedWindow:
     each layer with the windows' tokens of all those videos, row after row.  The keys and values
     of a window chunk are written anew each step; the last ones, from the step before the chunk
     leaves the window, are what later chunks read.  ``fork`` continues a video in two ways: the
-    pages are shared until one of the two writes to them."""
+    pages are shared until one of the two writes to them.
+
+    A step says where its videos' tokens lie as ``begin`` found it: once one of them has been forked,
+    has slid or was closed, or ``compact`` has moved pages, ``run`` refuses it (ValueError), since the
+    pages may be shared or another video's by then."""
 
     def __init__(self, hq: int, hkv: int, d: int, frames: int, height: int, width: int, window: int,
                  cache_chunks: int, kv_range: int, videos: int, layers: int = 1, rope_base=(1e4, 1e4, 1e4),
@@ -161,6 +166,8 @@ class PagedWindow:
         self._videos: Dict[int, PipelinedWindow] = {}
         self._first: Dict[int, int] = {}
         self._oldest: Dict[int, int] = {}    # the first chunk that was ever in the window
+        self._moved: Dict[int, int] = {}     # the event after which steps of the video are out of date
+        self._events = 0
         self.pending_copies: List[Tuple[int, int]] = []   # that the tables count on already
 
     # ------------------------------------------------------------------ videos
@@ -172,7 +179,14 @@ class PagedWindow:
         video = self.pool.open()
         self._videos[video], self._first[video] = self._schedule(), first_chunk
         self._oldest[video] = first_chunk
+        self._out_of_date(video)
         return video
+
+    def _out_of_date(self, *videos: int) -> None:
+        """Steps of these videos begun so far no longer hold."""
+        self._events += 1
+        for v in videos:
+            self._moved[v] = self._events
 
     def _get(self, video: int) -> PipelinedWindow:
         if video not in self._videos:
@@ -189,6 +203,7 @@ class PagedWindow:
     def slide(self, video: int) -> None:
         """The window moves on by one chunk; pages that no window chunk can see any more go back."""
         self._get(video)
+        self._out_of_date(video)
         self._first[video] += 1
         self.pool.release_before(video, (self._first[video] - self.cache_chunks) * self.chunk_tokens)
 
@@ -198,18 +213,21 @@ class PagedWindow:
         self._videos[new], self._first[new] = self._schedule(), self._first[video]
         self._oldest[new] = self._oldest[video]
         self._videos[new].transitions.update(old.transitions)
+        self._out_of_date(video, new)
         return new
 
     def close_video(self, video: int) -> None:
         self._get(video)
         self.pool.close(video)
-        del self._videos[video], self._first[video], self._oldest[video]
+        del self._videos[video], self._first[video], self._oldest[video], self._moved[video]
 
     def compact(self, stream=None) -> int:
-        """Move the pages in use to the front of the pool; returns how many moved.  Steps begun
-        before hold old tables: begin them again."""
+        """Move the pages in use to the front of the pool; returns how many moved.  If any did, steps
+        begun before hold old tables: begin them again."""
         self._copy_pending(stream)
         self.pending_copies = self.pool.compact()
+        if self.pending_copies:
+            self._out_of_date(*self._videos)
         return self._copy_pending(stream)
 
     def _copy_pending(self, stream) -> int:
@@ -263,11 +281,15 @@ class PagedWindow:
             pos[:, 0] += begun.repeat_interleave(per)
             return PagedStep(tuple(videos), n, torch.from_numpy(table).to(dev),
                              torch.arange(0, n + 1, per, dtype=i32, device=dev), small[:len(starts)],
-                             torch.arange(0, n + 1, C, dtype=i32, device=dev), keys[0], keys[1], keys[2], pos)
+                             torch.arange(0, n + 1, C, dtype=i32, device=dev), keys[0], keys[1], keys[2], pos,
+                             tuple(self._moved[v] for v in videos))
 
     def run(self, step: PagedStep, q, k, v, *, layer: int = 0, q_gain=None, k_gain=None, o=None, lse=None,
             stream=None):
         """Write k, v [rows, Hkv, D] of the step's windows and attend q [rows, Hq, D]; returns o."""
+        if step.made != tuple(self._moved.get(v) for v in step.videos):
+            raise ValueError("the step is out of date: one of its videos was forked, slid or closed, or pages were "
+                             "compacted; begin it again")
         if k.shape[0] != step.rows or q.shape[0] != step.rows:
             raise ValueError(f"expected {step.rows} rows of q, k and v")
         self.cache.write(k, v, step.table, step.row_off, step.start, pos=step.pos, k_gain=k_gain, layer=layer,
