@@ -256,7 +256,7 @@ class PagedWindow:
             starts.append(first * C - base)
             for p, r in enumerate(self._videos[v].ranges(first)):
                 seen.append((b, (first + p - min(r, first + p - oldest)) * C - base, (first + p + 1) * C - base))
-        rows = [self.pool.row(v)[skip:] for v, skip in zip(videos, bases)]
+        rows = [self.pool.row(v, skip) for v, skip in zip(videos, bases)]
         table = np.full((len(rows), max((len(r) for r in rows), default=0)), -1, np.int32)
         for b, r in enumerate(rows):
             table[b, :len(r)] = r
