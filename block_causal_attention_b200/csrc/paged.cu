@@ -436,6 +436,12 @@ int launch_join(const PagedArgs &a, cudaStream_t stream) {
     return cudaLaunchKernelEx(&cfg, paged_join_kernel<D, T>, a) == cudaSuccess ? BCA_OK : BCA_ERR_CUDA;
 }
 
+// ------------------------------------------------------------------ the status word
+
+// Takes one reported bit back.  Kernels of other streams may set bits at any time, so the word is
+// never written as a whole.
+__global__ void paged_status_clear_kernel(int *status, int bit) { atomicAnd(status, ~bit); }
+
 // ------------------------------------------------------------------ by head size and type
 
 template <typename F>
@@ -538,6 +544,11 @@ int launch_paged_copy(const PagedCache &c, const int32_t *pairs, int64_t n, void
         at += m;
     }
     return BCA_OK;
+}
+
+int launch_paged_status_clear(const PagedCache &c, int bit, cudaStream_t stream) {
+    paged_status_clear_kernel<<<1, 1, 0, stream>>>(c.d_status, bit);
+    return cudaGetLastError() == cudaSuccess ? BCA_OK : BCA_ERR_CUDA;
 }
 
 int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream_t stream) {

@@ -76,6 +76,7 @@ int launch_paged_write(const PagedCache &c, const PagedWriteIO &io, cudaStream_t
 int launch_paged_copy(const PagedCache &c, const int32_t *pairs, int64_t n, void *k_pages, void *v_pages,
                       cudaStream_t stream);
 int launch_paged_attend(const PagedCache &c, const PagedAttendIO &io, cudaStream_t stream);
+int launch_paged_status_clear(const PagedCache &c, int bit, cudaStream_t stream);
 
 struct PagedArgs;
 int prepare_paged_rows(const PagedCache &c);

@@ -195,12 +195,18 @@ int bca_paged_status(bca_paged_t cache, void *stream) {
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     if (cudaMemcpyAsync(&h, c.d_status, sizeof(int), cudaMemcpyDeviceToHost, s) != cudaSuccess) return BCA_ERR_CUDA;
     if (cudaStreamSynchronize(s) != cudaSuccess) return BCA_ERR_CUDA;
-    if (h == 0) return BCA_OK;
-    if (cudaMemsetAsync(c.d_status, 0, sizeof(int), s) != cudaSuccess) return BCA_ERR_CUDA;
-    if (cudaStreamSynchronize(s) != cudaSuccess) return BCA_ERR_CUDA;
-    return (h & bca::kPagedTimeout)     ? BCA_ERR_DEVICE_TIMEOUT
-           : (h & bca::kPagedWorkspace) ? BCA_ERR_INVALID_ARGUMENT
-                                        : BCA_ERR_BAD_PAGE;
+    // one kind of error a call; what else there is, or comes up meanwhile, is left for the next
+    const struct {
+        int bit, code;
+    } kinds[] = {{bca::kPagedTimeout, BCA_ERR_DEVICE_TIMEOUT},
+                 {bca::kPagedWorkspace, BCA_ERR_INVALID_ARGUMENT},
+                 {bca::kPagedNoPage, BCA_ERR_BAD_PAGE}};
+    for (const auto &k : kinds)
+        if (h & k.bit) {
+            if (bca::launch_paged_status_clear(c, k.bit, s) != BCA_OK) return BCA_ERR_CUDA;
+            return cudaStreamSynchronize(s) == cudaSuccess ? k.code : BCA_ERR_CUDA;
+        }
+    return BCA_OK;
 }
 
 }  // extern "C"

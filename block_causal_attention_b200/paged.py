@@ -152,9 +152,10 @@ class PagedCache:
             return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def status(self, stream=None) -> int:
-        """Status of the work on `stream`, waited for: BCA_OK, BCA_ERR_DEVICE_TIMEOUT,
-        BCA_ERR_INVALID_ARGUMENT when overlapping calls shared a workspace and noticed it, or
-        BCA_ERR_BAD_PAGE when a written token had no page.  Reading it clears it."""
+        """Status of the cache's calls, those on `stream` waited for and those of other streams as
+        far as they have run: BCA_OK, BCA_ERR_DEVICE_TIMEOUT, BCA_ERR_INVALID_ARGUMENT when
+        overlapping calls shared a workspace and noticed it, or BCA_ERR_BAD_PAGE when a written
+        token had no page.  Reading clears what is returned; another kind is left for the next call."""
         if stream is None and not self.host_only:
             stream = torch.cuda.current_stream(self.device)
         return int(self._lib.bca_paged_status(self._h, self._stream(stream)))

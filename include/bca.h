@@ -432,7 +432,10 @@ int bca_paged_attend(bca_paged_t cache, const void *q, int64_t nq, const int32_t
 
 /* Device status word of the cache, as bca_status: a wait that ran out
  * (BCA_ERR_DEVICE_TIMEOUT), overlapping calls that were given one workspace and noticed it
- * (BCA_ERR_INVALID_ARGUMENT), or written tokens without a page (BCA_ERR_BAD_PAGE). */
+ * (BCA_ERR_INVALID_ARGUMENT), or written tokens without a page (BCA_ERR_BAD_PAGE).  The word is
+ * one for all streams: it tells of every call on `stream`, which is waited for, and of those of
+ * other streams that have run so far.  A call reports one kind of error and clears that one; call
+ * until BCA_OK to see them all. */
 int bca_paged_status(bca_paged_t cache, void *stream);
 
 const char *bca_error_string(int code);
