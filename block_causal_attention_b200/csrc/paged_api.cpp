@@ -67,6 +67,8 @@ int bca_paged_create(const bca_paged_desc *desc, bca_paged_t *out) {
         if (cudaGetDevice(&c.device) != cudaSuccess) rc = BCA_ERR_CUDA;
         else if (cudaMalloc(reinterpret_cast<void **>(&c.d_status), 256) != cudaSuccess) rc = BCA_ERR_NO_MEMORY;
         else if (cudaMemset(c.d_status, 0, 256) != cudaSuccess) rc = BCA_ERR_CUDA;
+        // (asynchronous, on a stream that streams made non-blocking do not wait for)
+        else if (cudaStreamSynchronize(cudaStreamLegacy) != cudaSuccess) rc = BCA_ERR_CUDA;
         else rc = bca::prepare_paged(c);
     }
     if (rc != BCA_OK) {
