@@ -45,7 +45,8 @@ EXPORTS = ("bca_plan_create", "bca_plan_destroy", "bca_plan_get_info", "bca_plan
            "bca_bwd_ex", "bca_attn_merge", "bca_k_prologue", "bca_k_prologue_bwd",
            "bca_profile_enable",
            "bca_profile_read", "bca_status", "bca_paged_create", "bca_paged_destroy", "bca_paged_pool_bytes",
-           "bca_paged_write", "bca_paged_copy", "bca_paged_workspace_bytes", "bca_paged_attend",
+           "bca_paged_write", "bca_paged_copy", "bca_paged_workspace_bytes",
+           "bca_paged_max_workspace_bytes", "bca_paged_attend",
            "bca_paged_status", "bca_error_string")
 BCA_KERNEL_KV_IMAGE = 0
 BCA_KERNEL_FWD = 1
@@ -150,6 +151,8 @@ def lib() -> ctypes.CDLL:
         L.bca_paged_copy.restype = i32
         L.bca_paged_workspace_bytes.argtypes = [vp, i64, i32, i32]
         L.bca_paged_workspace_bytes.restype = ctypes.c_size_t
+        L.bca_paged_max_workspace_bytes.argtypes = [vp]
+        L.bca_paged_max_workspace_bytes.restype = ctypes.c_size_t
         L.bca_paged_attend.argtypes = [vp, vp, i64, vp, vp, vp, vp, vp, i32, i32, vp, vp, vp, vp, i32, i32, vp, vp,
                                        vp, vp]
         L.bca_paged_attend.restype = i32

@@ -477,9 +477,19 @@ PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices, int width) {
     return s;
 }
 
+static size_t shares_bytes(const PagedCache &c, int rows) {
+    return paged_shares(rows) * (kPagedJoinBytes + 2 * (size_t)rows * (c.d + 2) * sizeof(float));
+}
+
 size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices, int width) {
     const PagedShape s = paged_shape(c, nq, slices, width);
-    return s.items > 0 ? 0 : paged_shares(s.rows) * (kPagedJoinBytes + 2 * (size_t)s.rows * (c.d + 2) * sizeof(float));
+    return s.items > 0 ? 0 : shares_bytes(c, s.rows);
+}
+
+size_t paged_max_workspace_bytes(const PagedCache &c) {
+    size_t most = 0;
+    for (int rows : {16, 32, kPagedNarrowRows, kPagedTileRows}) most = std::max(most, shares_bytes(c, rows));
+    return most;
 }
 
 int prepare_paged(const PagedCache &c) {

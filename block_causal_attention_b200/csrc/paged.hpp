@@ -70,6 +70,7 @@ struct PagedShape {
 };
 PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices, int width);
 size_t paged_workspace_bytes(const PagedCache &c, int64_t nq, int slices, int width);
+size_t paged_max_workspace_bytes(const PagedCache &c);  // of any sizes
 
 int prepare_paged(const PagedCache &c);
 int launch_paged_write(const PagedCache &c, const PagedWriteIO &io, cudaStream_t stream);

@@ -163,6 +163,10 @@ size_t bca_paged_workspace_bytes(bca_paged_t cache, int64_t nq, int32_t slices, 
     return bca::paged_workspace_bytes(cache->cache, nq, slices, width);
 }
 
+size_t bca_paged_max_workspace_bytes(bca_paged_t cache) {
+    return cache ? bca::paged_max_workspace_bytes(cache->cache) : 0;
+}
+
 int bca_paged_attend(bca_paged_t cache, const void *q, int64_t nq, const int32_t *pos, const float *q_gain,
                      const void *k_pages, const void *v_pages, const int32_t *table, int32_t seqs, int32_t width,
                      const int32_t *off, const int32_t *seq, const int32_t *k_begin, const int32_t *k_end,

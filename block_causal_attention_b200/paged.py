@@ -139,8 +139,13 @@ class PagedCache:
         return o
 
     def workspace_bytes(self, nq: int, slices: int, width: int) -> int:
-        """Bytes of workspace of an ``attend`` call: rows of q, slices, columns of the table."""
+        """Bytes of workspace of an ``attend`` call: rows of q, slices, columns of the table.  A call
+        of fewer rows or slices can need more."""
         return int(self._lib.bca_paged_workspace_bytes(self._h, nq, slices, width))
+
+    def max_workspace_bytes(self) -> int:
+        """What no ``attend`` call of this cache passes, whatever its sizes."""
+        return int(self._lib.bca_paged_max_workspace_bytes(self._h))
 
     def alloc_workspace(self, nq: int, slices: int, width: int, stream=None):
         """Workspace of an ``attend`` call of these sizes, on its stream.  Calls that may overlap

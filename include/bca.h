@@ -420,10 +420,15 @@ int bca_paged_copy(bca_paged_t cache, const int32_t *pairs, int64_t n, void *k_p
  * Rows that see no key get O = 0 and LSE = -inf (so does a row whose every score is -inf), rows
  * with a score that is NaN get NaN in O and LSE; rows of q outside every slice are neither
  * read nor written.  What pages hold outside a row's own keys never reaches the row, NaN and
- * infinities included.  workspace: bca_paged_workspace_bytes bytes (which may be 0: NULL then),
- * 16-byte aligned; calls that may overlap on the GPU need one each.  Results do not depend on timing: the same call
- * gives the same bits. */
+ * infinities included.  workspace: bca_paged_workspace_bytes bytes (which may be 0: NULL then) for
+ * the call's own nq, slices and width, 16-byte aligned; calls that may overlap on the GPU need one
+ * each.  A buffer that is kept for calls of several sizes needs bca_paged_max_workspace_bytes: the
+ * tiles, and with them the workspace, go by the rows of an average slice, so a call of fewer slices
+ * or rows can need more than a larger one, and the size given is not checked (it is not an argument).
+ * Results do not depend on timing: the same call gives the same bits. */
 size_t bca_paged_workspace_bytes(bca_paged_t cache, int64_t nq, int32_t slices, int32_t width);
+/* What no bca_paged_attend call of this cache passes: 12 to 23 MB by head dimension. */
+size_t bca_paged_max_workspace_bytes(bca_paged_t cache);
 int bca_paged_attend(bca_paged_t cache, const void *q, int64_t nq, const int32_t *pos, const float *q_gain,
                      const void *k_pages, const void *v_pages, const int32_t *table, int32_t seqs,
                      int32_t width, const int32_t *off, const int32_t *seq, const int32_t *k_begin,
