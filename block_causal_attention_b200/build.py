@@ -1,11 +1,14 @@
-"""Build libbca.so (the C-ABI library) in-tree with nvcc for sm_100a, and the Python module
-that calls its paged cache."""
+"""Build libbca.so (the C-ABI library) in-tree with nvcc for sm_100a, and, where there is a PyTorch
+to build it for, the Python module that calls the library's paged cache."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
 import shutil
 import subprocess
+import sysconfig
+import warnings
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -35,10 +38,17 @@ def _stale(target: str, deps) -> bool:
     return any(os.path.getmtime(d) > t for d in deps)
 
 
+def _binding_lacks() -> str:
+    """What the module's build needs and is not there, or nothing.  The library needs none of it."""
+    if importlib.util.find_spec("torch") is None:
+        return "PyTorch"
+    if not os.path.exists(os.path.join(sysconfig.get_path("include"), "Python.h")):
+        return "Python's headers"
+    return ""
+
+
 def _binding_command(target: str) -> list:
     """The Python module over torch tensors (csrc/paged_binding.cpp), against libbca.so."""
-    import sysconfig
-
     import torch
     from torch.utils import cpp_extension as ext
     lib = os.path.join(os.path.dirname(torch.__file__), "lib")
@@ -81,7 +91,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         run([nvcc, *ARCH, "-shared", "-o", tmp, *objs, "-lpthread"])
         os.replace(tmp, LIB)
     header = os.path.join(ROOT, "include", "bca.h")
-    if force or _stale(BINDING, [os.path.join(CSRC, "paged_binding.cpp"), header]):
+    lacks = _binding_lacks()
+    if lacks:
+        warnings.warn(f"libbca.so is built; the module of the paged cache is not: {lacks} not found. "
+                      "PagedCache needs it, plans and the C ABI do not.")
+    elif force or _stale(BINDING, [os.path.join(CSRC, "paged_binding.cpp"), header]):
         tmp = BINDING + f".tmp{os.getpid()}"
         run(_binding_command(tmp))
         os.replace(tmp, BINDING)
