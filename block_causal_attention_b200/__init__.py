@@ -251,7 +251,7 @@ class Plan:
 
 
 def __getattr__(name):
-    # on first use: the module needs PyTorch, which the host side of a plan does not
+    # on first use: most users of plans need neither
     if name in ("PagedCache", "PagePool"):
         from . import paged
         return getattr(paged, name)

@@ -12,7 +12,6 @@ import heapq
 from typing import Dict, List, Optional, Sequence
 
 import numpy as np
-import torch
 
 from . import _abi
 
@@ -30,6 +29,7 @@ class PagedCache:
     def __init__(self, hq: int, hkv: int, d: int, pages: int, *, layers: int = 1, dtype=None,
                  rope_base=(1e4, 1e4, 1e4), eps: float = 1e-6, o_fp32: bool = False, k_pages=None, v_pages=None,
                  host_only: bool = False, test_force_timeout: bool = False):
+        import torch   # here and below: PagePool needs no PyTorch
         dtype = torch.bfloat16 if dtype is None else dtype
         if dtype not in (torch.bfloat16, torch.float16):
             raise ValueError(f"dtype: expected torch.bfloat16 or torch.float16, got {dtype}")
@@ -50,7 +50,7 @@ class PagedCache:
         self.k_shape = (self.layers, self.pages, self.hkv, self.d // 8, PAGE, 8)
         self.v_shape = (self.layers, self.pages, self.hkv, PAGE // 8, self.d, 8)
         self.pool_bytes = int(self._lib.bca_paged_pool_bytes(self._h))
-        self._pools: Dict[str, torch.Tensor] = {}
+        self._pools: Dict[str, "torch.Tensor"] = {}
         self.device = None
         if self.host_only:
             return
@@ -105,6 +105,7 @@ class PagedCache:
         """Make page pairs[i, 1] a copy of page pairs[i, 0], in every layer.  pairs: [n, 2] on
         the host (a CPU tensor, an array or a list), read before the call returns.  A page may
         be written once, and none that is written may be read."""
+        import torch
         c = self._on_gpu()
         if not (isinstance(pairs, torch.Tensor) and pairs.dtype is torch.int32 and pairs.is_contiguous()):
             if isinstance(pairs, torch.Tensor) and pairs.is_cuda:
@@ -150,6 +151,7 @@ class PagedCache:
     def alloc_workspace(self, nq: int, slices: int, width: int, stream=None):
         """Workspace of an ``attend`` call of these sizes, on its stream.  Calls that may overlap
         on the GPU (two streams, two captured graphs replayed side by side) need one each."""
+        import torch
         n = max(16, self.workspace_bytes(nq, slices, width))
         if isinstance(stream, int):
             stream = torch.cuda.ExternalStream(stream, device=self.device)
@@ -161,6 +163,7 @@ class PagedCache:
         far as they have run: BCA_OK, BCA_ERR_DEVICE_TIMEOUT, BCA_ERR_INVALID_ARGUMENT when
         overlapping calls shared a workspace and noticed it, or BCA_ERR_BAD_PAGE when a written
         token had no page.  Reading clears what is returned; another kind is left for the next call."""
+        import torch
         if stream is None and not self.host_only:
             stream = torch.cuda.current_stream(self.device)
         return int(self._lib.bca_paged_status(self._h, self._stream(stream)))

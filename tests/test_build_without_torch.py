@@ -1,5 +1,5 @@
-"""What needs no PyTorch works without it: building the library and plans' host side.  Each check
-runs in a process of its own in which importing torch fails."""
+"""What needs no PyTorch works without it: building the library, plans' host side and
+the page bookkeeping.  Each check runs in a process of its own in which importing torch fails."""
 import os
 import subprocess
 import sys
@@ -29,3 +29,19 @@ def test_the_library_is_built_and_used(tmp_path):
         print("done")
         """)
     assert out.endswith("done\n") and "paged" in err and "PyTorch" in err
+
+
+def test_page_bookkeeping_and_import_star():
+    out, _ = without_torch("""
+        from block_causal_attention_b200 import *
+        p = PagePool(4)
+        a = p.open()
+        assert p.grow(a, 0, 300) == [] and p.row(a) == [0, 1, 2]
+        from block_causal_attention_b200.streaming import PipelinedWindow
+        assert PipelinedWindow(2, 1, 24, 1, 8, 8, 2, 1, 1, host_only=True).ranges(1) == (1, 1)
+        try:
+            PagedCache(2, 1, 24, 4, host_only=True)
+        except ImportError:
+            print("done")
+        """)
+    assert out.endswith("done\n")
