@@ -5,6 +5,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import re
 
 import numpy as np
 
@@ -172,6 +173,11 @@ def paged_binding():
     except ImportError as e:
         raise ImportError(f"the module _paged_binding is not built for this PyTorch ({e}); run "
                           "`python -m block_causal_attention_b200.build --force`") from e
+    import torch
+    # (the release numbers alone: a source build's 2.11.0a0+git... says 2.11.0 in its headers)
+    if _paged_binding.torch_version != re.match(r"[0-9.]*[0-9]", torch.__version__).group():
+        raise ImportError(f"the module _paged_binding was built for PyTorch {_paged_binding.torch_version}, this is "
+                          f"{torch.__version__}; run `python -m block_causal_attention_b200.build`")
     return _paged_binding
 
 

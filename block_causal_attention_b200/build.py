@@ -3,10 +3,12 @@ to build it for, the Python module that calls the library's paged cache."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.metadata
 import importlib.util
 import os
 import shutil
 import subprocess
+import sys
 import sysconfig
 import warnings
 
@@ -16,6 +18,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libbca.so")
 BINDING = os.path.join(PKG, "_paged_binding.so")
+BINDING_FOR = os.path.join(BUILD, "paged_binding.for")   # what BINDING was compiled against
 SOURCES = ["api.cpp", "plan.cpp", "fwd.cu", "fwd_static.cu", "bwd.cu", "cp_passes.cu", "paged_api.cpp", "paged.cu",
            "paged_rows.cu", "paged_tiles.cu"]
 HEADERS = ["plan.hpp", "kernels.hpp", "sm100.cuh", "prologue.cuh", "paged.hpp", "paged_device.cuh", "paged_mma.cuh"]
@@ -36,6 +39,13 @@ def _stale(target: str, deps) -> bool:
         return True
     t = os.path.getmtime(target)
     return any(os.path.getmtime(d) > t for d in deps)
+
+
+def _read(path: str) -> str:
+    if not os.path.exists(path):
+        return ""
+    with open(path) as f:
+        return f.read()
 
 
 def _binding_lacks() -> str:
@@ -92,16 +102,18 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         os.replace(tmp, LIB)
     header = os.path.join(ROOT, "include", "bca.h")
     lacks = _binding_lacks()
+    versions = "" if lacks else f"torch {importlib.metadata.version('torch')}, Python {sys.version}\n"
     if lacks:
         warnings.warn(f"libbca.so is built; the module of the paged cache is not: {lacks} not found. "
                       "PagedCache needs it, plans and the C ABI do not.")
-    elif force or _stale(BINDING, [os.path.join(CSRC, "paged_binding.cpp"), header]):
+    elif force or _stale(BINDING, [os.path.join(CSRC, "paged_binding.cpp"), header]) or _read(BINDING_FOR) != versions:
         tmp = BINDING + f".tmp{os.getpid()}"
         run(_binding_command(tmp))
         os.replace(tmp, BINDING)
+        with open(BINDING_FOR, "w") as f:
+            f.write(versions)
     return LIB
 
 
 if __name__ == "__main__":
-    import sys
     print(build(force="--force" in sys.argv, verbose="-v" in sys.argv))
