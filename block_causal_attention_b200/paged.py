@@ -18,6 +18,15 @@ from . import _abi
 PAGE = _abi.BCA_PAGE_TOKENS
 
 
+def on_stream(stream, device):
+    """The context of a stream given as a torch stream, as a number (cudaStream_t), or as None: the
+    current one."""
+    import torch
+    if isinstance(stream, int):
+        stream = torch.cuda.ExternalStream(stream, device=device)
+    return torch.cuda.stream(stream)
+
+
 class PagedCache:
     """A pool of pages for `layers` layers and the operators on it: ``write`` new tokens,
     ``copy_pages`` and ``attend``.
@@ -153,9 +162,7 @@ class PagedCache:
         on the GPU (two streams, two captured graphs replayed side by side) need one each."""
         import torch
         n = max(16, self.workspace_bytes(nq, slices, width))
-        if isinstance(stream, int):
-            stream = torch.cuda.ExternalStream(stream, device=self.device)
-        with torch.cuda.stream(stream):   # its next user is behind this call; None: the current one
+        with on_stream(stream, self.device):   # its next user is behind this call
             return torch.empty(n, dtype=torch.uint8, device=self.device)
 
     def status(self, stream=None) -> int:

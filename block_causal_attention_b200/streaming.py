@@ -266,9 +266,11 @@ class PagedWindow:
         """Pages for the windows of `videos` (copied first where they are shared) and the step's
         device data."""
         import torch
+
+        from .paged import on_stream
         self._copy_pending(stream)   # of a step that found no page: before new ones can build on them
         table, starts, seen = self.layout(videos)
-        with torch.cuda.stream(stream):
+        with on_stream(stream, self.cache.device):
             self._copy_pending(stream)
             dev, C, per = self.cache.device, self.chunk_tokens, self.window * self.chunk_tokens
             n, i32 = len(videos) * per, torch.int32
