@@ -17,8 +17,9 @@ namespace {
 // ------------------------------------------------------------------ writing new tokens
 //
 // k_hat = R(pos) (gain * k / sqrt(mean k^2 + eps)) in fp16, v as it is, both into the layout
-// of the pages.  Bound by memory: 4 D Hkv bytes read and as many written a token.  Measured:
-// 43,200 tokens of 8 heads, D = 48, 28.4 us, 4.7 TB/s (2.3 waves of blocks, each 50 KB on the way).
+// of the pages.  Bound by memory: 4 D Hkv bytes read and as many written a token.  Measured on
+// the device: 43,200 tokens of 8 heads, D = 48, 27.8 us, 4.8 TB/s (2.3 waves of blocks, each 50 KB on
+// the way).
 //
 // A block takes the (up to) 32 tokens of one 32-aligned stretch of a page and up to eight KV
 // heads.  Their rows come to shared memory by bulk copies, one a token, issued before anything
@@ -233,8 +234,8 @@ __global__ void __launch_bounds__(kWriteThreads) paged_write_kernel(const __grid
 //
 // The page numbers travel as kernel arguments (at most 32,764 bytes of them), so the call
 // needs neither a device buffer nor a copy that would have to outlive it.  Bound by memory:
-// a block moves 16 KB of a page, four 16-byte loads in flight a thread.  Measured: 805 MB in
-// 123.6 us, 6.5 TB/s; 48 pages of 196 KB in 2.9 us.
+// a block moves 16 KB of a page, four 16-byte loads in flight a thread.  Measured on
+// the device: 805 MB in 123.5 us, 6.5 TB/s; 48 pages of 196 KB in 3.1 us.
 
 constexpr int kCopyThreads = 256;
 constexpr int kCopyUnits = 1024;  // 16-byte units a block
@@ -467,6 +468,10 @@ int by_type(const PagedCache &c, F &&f) {
 //   384-row tiles       90 / 110   90 / 111   90 / 112   92 / 114  121 / 154  227 / 286   36 / 45   52 / 72
 // and on chunks, 128- against 384-row tiles: the 4.5B window 1,016 / 876 us, half a 720p chunk
 // 2,270 / 2,220, ragged chunks of several streams 408 / 322.
+// All of these are slices of like sizes.  A call that mixes sizes gets the average's tiles for all:
+// 31 single tokens over 1,000 to 31,000 keys beside a chunk of 2,001 over 5,000 (128 heads of 8,
+// D = 48) take 1,011 us in one call, 140 and 673 in two; 1,023 single tokens over 100 to 1,100 keys
+// beside a chunk of 300 over 8,000 take 1,562, against 463 and 150.  Two calls are the way there.
 PagedShape paged_shape(const PagedCache &c, int64_t nq, int slices, int width) {
     const int64_t group = c.hq / c.hkv, rows = nq * group / std::max(slices, 1);
     PagedShape s = {rows <= 16 ? 16 : rows <= 64 ? 32 : rows <= 256 ? kPagedNarrowRows : kPagedTileRows, 0};

@@ -1,7 +1,7 @@
 // The paged cache's operators as Python functions over torch tensors (module _paged_binding):
 // argument checks, allocation and the calls of include/bca.h.  A single token's attention takes
-// the GPU 9 us; the same checks by interpreter steps and ctypes took 19 us a call, so here they
-// are compiled.
+// the GPU 6.1 us (one token of 128 heads over 1,536 keys, D = 24); the same checks by interpreter
+// steps and ctypes took 19 us a call, compiled they take 7.
 #define PY_SSIZE_T_CLEAN
 #include <Python.h>
 

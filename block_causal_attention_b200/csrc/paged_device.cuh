@@ -385,8 +385,9 @@ template <>
 struct Io<__half> {
     static constexpr bool kF16 = true;
     // The reference is put 6 below the running maximum: P then lies between 2^-24 (fp16's
-    // smallest) and 2^6, up to 2^14 before the reference moves, below fp16's 65504; without
-    // it a key 2^-14 below the largest would already lose bits of its P.
+    // smallest) and 2^6, and before the reference moves up to 2^14 in the few-row kernel (kLazy)
+    // and 2^15 in the many-row one (kTop), below fp16's 65504; without it a key 2^-14 below the
+    // largest would already lose bits of its P.
     static constexpr float kShift = 6.f;
     static constexpr float kTop = 32768.f;  // no weight above 2^15, below fp16's 65504
     static __device__ __forceinline__ float2 unpack(uint32_t u) {
@@ -419,9 +420,13 @@ __device__ __forceinline__ float2 paged_cos_sin(int32_t position, uint64_t turns
     sincospif((float)paged_turn(position, turns) * 4.656612873077393e-10f, &cs.y, &cs.x);  // half turns: 2^-31
     return cs;
 }
-// The same from the special-function unit, for queries: they are rounded to fp16 (2^-12 of a
-// value) and used once, so an error of 2^-20 does not count, while the queries of an item are
-// 9,216 angles that stand before its first score (they took 6 us of every block's life).
+// The same from the special-function unit, for queries, to 2^-20.5 of the pair's length each: the
+// queries of an item are 9,216 angles that stand before its first score (sincospif took 6 us of
+// every block's life).  With bf16 values the query is then rounded to fp16, half a step 2^-11, and
+// the angle's error does not show.  With fp16 values, whose queries keep what that rounding leaves,
+// it is the largest error of a score, 2^-19.6 of |q||k| / sqrt(D); at the norms that QK-Norm gives
+// (sqrt(D) each, D = 48) that moves a weight by 9e-6 of itself, beside the 2^-11 by which its own
+// rounding to fp16 may.
 __device__ __forceinline__ float2 paged_cos_sin_fast(int32_t position, uint64_t turns) {
     const float x = (float)paged_turn(position, turns) * 1.4629180792671596e-9f;  // radians: 2 pi 2^-32
     return make_float2(__cosf(x), __sinf(x));

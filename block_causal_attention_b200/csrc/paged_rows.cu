@@ -9,9 +9,9 @@
 // flight: one block a multiprocessor, a ring of whole pages (a page's keys and values of one
 // head are two contiguous stretches, moved by two bulk copies) filled by one warp that runs
 // ahead over page and item borders.  Eight warps take 16 of a page's 128 tokens each; their
-// results meet once an item, so that one page is enough work for all of them.  Measured: one
-// token of 128 heads over 172,800 keys of 8 KV heads, D = 48, 49 us (5.4 TB/s with the launch and
-// the joining pass, about 8 us); 32 tokens over 512,000 keys 139 us, 5.9 TB/s.
+// results meet once an item, so that one page is enough work for all of them.  Measured on the
+// device: one token of 128 heads over 172,800 keys of 8 KV heads, D = 48, 49 us (5.4 TB/s with the
+// launch and the joining pass, about 8 us); 32 tokens over 512,000 keys 142 us, 5.7 TB/s.
 //
 // The layout of the pages is that of the 8 x 8 matrices that ldmatrix reads: 8 tokens x 8
 // channels of K and 8 channels x 8 tokens of V lie in 128 contiguous bytes, so both operands
@@ -169,7 +169,8 @@ __global__ void __launch_bounds__(kThreads, 1) paged_rows_kernel(const __grid_co
         // queries: QK-Norm and RoPE, fp16 (|q_hat| <= sqrt(D) max|gain|; 11 bits of significand
         // against bf16's 8), with what the rounding left where values are fp16.  The
         // softmax scale is applied to the scores in fp32 instead, so that bf16 queries given
-        // post-prologue stay exact.
+        // post-prologue stay exact in fp16's normal range (below 2^-14 their last bits go, below
+        // 2^-25 all of them).
         for (int r = threadIdx.x >> 3; r < R; r += kWarps * 4) {
             const int e = lane & 7;
             const bool live = r < x.left;  // the same for the eight lanes of a row

@@ -16,9 +16,10 @@
 //   - no running maximum where every row sees the whole page: the sums of the weights, needed
 //     anyway, tell when the reference has to move (3.1 -> 2.4 ms at the size below).
 // The same instructions without barriers take 1,280 cycles a 128 x 128 tile at D = 24 and 1,480
-// at D = 48 (1,024 of them exponentials), this kernel 1,400 and 1,760.  Measured: 10,800 tokens
-// of 16 heads over 32,400 keys, D = 48, 2.18 ms, 492 TFLOP/s, the special-function units 57 %
-// and the tensor pipe 53 % busy; 6,144 tokens of 32 heads over 13,824 keys, D = 24, 0.88 ms.
+// at D = 48 (1,024 of them exponentials), this kernel 1,400 and 1,760.  Measured on the
+// device: 10,800 tokens of 16 heads over 32,400 keys, D = 48, 2.20 ms, 489 TFLOP/s, the
+// special-function units 57 % and the tensor pipe 53 % busy; 6,144 tokens of 32 heads over 13,824
+// keys, D = 24, 0.88 ms.  (The dense forward of this library, P V by tcgen05, takes 2.08 and 1.08 ms.)
 #include <cuda_runtime.h>
 
 #include <type_traits>

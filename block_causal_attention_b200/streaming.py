@@ -264,7 +264,9 @@ class PagedWindow:
 
     def begin(self, videos: Sequence[int], stream=None) -> PagedStep:
         """Pages for the windows of `videos` (copied first where they are shared) and the step's
-        device data."""
+        device data: new tensors each time, uploaded from pageable memory, so this waits for the
+        stream and is not captured.  A graph of ``run`` reads the tensors of the step that it was
+        captured with; copy a later step's into them before it is replayed."""
         import torch
 
         from .paged import on_stream

@@ -345,7 +345,8 @@ int bca_status(bca_plan_t plan, void *stream);
  *   k_pages [pages][Hkv][D/8][128][8]  fp16: channel c of token s at [c/8][s][c%8]; keys are
  *                                      post-prologue (QK-Norm and RoPE applied), |x| < 65504
  *   v_pages [pages][Hkv][16][D][8]     io type (bf16, or fp16 with BCA_PAGED_FP16): channel c
- *                                      of token s at [s/8][c][s%8]
+ *                                      of token s at [s/8][c][s%8]; bf16 values with |x| < 2^90
+ *                                      (fp32 sums of values times weights up to 2^20)
  *
  * One pool holds the pages of one layer; a cache of L layers is L pools back to back.
  *
@@ -411,8 +412,11 @@ int bca_paged_copy(bca_paged_t cache, const int32_t *pairs, int64_t n, void *k_p
  * row r sees keys j with j <= k_end[i] - (off[i+1] - r).  Block-causal attention of a window
  * of chunks is one slice per chunk, a KV range is the slice's k_begin, one new token of each
  * of B videos is B slices of one row.  The new tokens' own keys have been written before.
+ * One tile size serves all slices of a call, chosen for the average one: single tokens and chunks
+ * are best given in calls of their own.
  *   q      : io type [nq][Hq][D];  o: the same, or fp32 with BCA_O_FP32
- *   pos    : device int32 [nq][3] or NULL: q is given post-prologue (|x| < 65504; q_gain NULL)
+ *   pos    : device int32 [nq][3] or NULL: q is given post-prologue (q_gain NULL).  Either way
+ *            post-prologue queries are held in fp16, so |x| < 65504 there
  *   off    : device int32 [slices + 1], non-decreasing;  seq: device int32 [slices], a value
  *            outside [0, seqs) is a slice that sees no key, or NULL: slice i reads row i;
  *   k_begin, k_end: device int32 [slices]
