@@ -32,7 +32,9 @@ class PagedCache:
     ``copy_pages`` and ``attend``.
 
     `dtype` (bf16 or fp16) is the type of q, k, v, o and the stored values; stored keys are
-    fp16, post-prologue.  `k_pages` / `v_pages` may be given (contiguous CUDA tensors of
+    fp16, post-prologue.  Calls run on `stream` (a torch stream, a number, or None: the current one)
+    with the cache's device current; tensors of another stream have to stay alive, and their
+    contents in place, until the call has run there.  `k_pages` / `v_pages` may be given (contiguous CUDA tensors of
     ``k_shape`` / ``v_shape``); otherwise they are allocated, uninitialised."""
 
     def __init__(self, hq: int, hkv: int, d: int, pages: int, *, layers: int = 1, dtype=None,
@@ -176,6 +178,8 @@ class PagedCache:
         return int(self._lib.bca_paged_status(self._h, self._stream(stream)))
 
     def close(self) -> None:
+        """Free the handle (the pools are tensors of their own).  A captured graph holds neither:
+        both have to outlive it."""
         if getattr(self, "_h", None) is not None and self._h.value:
             self._lib.bca_paged_destroy(self._h)
             self._h = _abi.ctypes.c_void_p()
@@ -196,7 +200,8 @@ class PagedCache:
 class PagePool:
     """Which page belongs to whom: sequences with page tables, shared pages counted, pages
     copied before a write when they are shared.  Host bookkeeping only; the copies it asks for
-    (lists of (from, to)) go to ``PagedCache.copy_pages``.
+    (lists of (from, to)) go to ``PagedCache.copy_pages``.  A page given back may be another
+    sequence's at once: work on both belongs on one stream, or on streams that the caller orders.
 
     Of a sequence it keeps the pages from the first one that is there on, so that calls cost what
     the pages in use cost, however far a window has slid (with an entry for every page there ever

@@ -143,7 +143,10 @@ class PagedWindow:
 
     A step says where its videos' tokens lie as ``begin`` found it: once one of them has been forked,
     has slid or was closed, or ``compact`` has moved pages, ``run`` refuses it (ValueError), since the
-    pages may be shared or another video's by then."""
+    pages may be shared or another video's by then.
+
+    Pages change hands between videos, so the calls of one window belong on one stream, or on
+    streams that the caller puts in the order of the calls."""
 
     def __init__(self, hq: int, hkv: int, d: int, frames: int, height: int, width: int, window: int,
                  cache_chunks: int, kv_range: int, videos: int, layers: int = 1, rope_base=(1e4, 1e4, 1e4),
@@ -265,8 +268,8 @@ class PagedWindow:
     def begin(self, videos: Sequence[int], stream=None) -> PagedStep:
         """Pages for the windows of `videos` (copied first where they are shared) and the step's
         device data: new tensors each time, uploaded from pageable memory, so this waits for the
-        stream and is not captured.  A graph of ``run`` reads the tensors of the step that it was
-        captured with; copy a later step's into them before it is replayed."""
+        stream and cannot be captured, and a graph captured over ``run`` goes on reading its own
+        step's."""
         import torch
 
         from .paged import on_stream

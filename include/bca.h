@@ -376,6 +376,7 @@ typedef struct {
 
 typedef struct bca_paged_s *bca_paged_t;
 
+/* A handle has to outlive the captured graphs that hold its calls, as their arrays have to. */
 int bca_paged_create(const bca_paged_desc *desc, bca_paged_t *out);
 void bca_paged_destroy(bca_paged_t cache);
 
