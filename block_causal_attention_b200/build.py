@@ -48,6 +48,14 @@ def _read(path: str) -> str:
         return f.read()
 
 
+def _torch_version() -> str:
+    try:
+        return importlib.metadata.version("torch")   # without the seconds that importing it takes
+    except importlib.metadata.PackageNotFoundError:  # a source tree on the path
+        import torch
+        return torch.__version__
+
+
 def _binding_lacks() -> str:
     """What the module's build needs and is not there, or nothing.  The library needs none of it."""
     if importlib.util.find_spec("torch") is None:
@@ -102,7 +110,7 @@ def build(force: bool = False, verbose: bool = False, extra_flags=()) -> str:
         os.replace(tmp, LIB)
     header = os.path.join(ROOT, "include", "bca.h")
     lacks = _binding_lacks()
-    versions = "" if lacks else f"torch {importlib.metadata.version('torch')}, Python {sys.version}\n"
+    versions = "" if lacks else f"torch {_torch_version()}, Python {sys.version}\n"
     if lacks:
         warnings.warn(f"libbca.so is built; the module of the paged cache is not: {lacks} not found. "
                       "PagedCache needs it, plans and the C ABI do not.")

@@ -36,3 +36,10 @@ def test_built_anew_for_another_pytorch(monkeypatch, tmp_path):
     assert len(made) == 2
     build.build()
     assert len(made) == 2
+
+
+def test_a_pytorch_that_was_not_installed_says_its_version_itself(monkeypatch):
+    def none(name):
+        raise importlib.metadata.PackageNotFoundError(name)
+    monkeypatch.setattr(importlib.metadata, "version", none)
+    assert build._torch_version() == torch.__version__
