@@ -143,7 +143,9 @@ class PagedWindow:
 
     A step says where its videos' tokens lie as ``begin`` found it: once one of them has been forked,
     has slid or was closed, or ``compact`` has moved pages, ``run`` refuses it (ValueError), since the
-    pages may be shared or another video's by then.
+    pages may be shared or another video's by then.  A step that was begun has to be run for all
+    layers: pages of the window that were shared are replaced by ``begin``, and not copied where each
+    of their tokens is about to be written.
 
     Pages change hands between videos, so the calls of one window belong on one stream, or on
     streams that the caller puts in the order of the calls."""
